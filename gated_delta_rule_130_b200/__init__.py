@@ -11,6 +11,8 @@ _BINDING_NAMES = {
     "chunk_fwd", "chunk_fwd_varlen", "chunk_fwd_varlen_workspace_size", "decode_step",
     "chunk_fwd_workspace_size", "chunk_fwd_path", "library_path", "chunk_bwd",
     "chunk_bwd_workspace_size", "chunk_fwd_cw", "chunk_fwd_cw_workspace_size", "decode_step_cw",
+    "decode_runs", "short_conv_fwd", "short_conv_bwd", "short_conv_bwd_workspace_size",
+    "rms_norm_fwd", "rms_norm_bwd", "rms_norm_bwd_workspace_size",
     "GdnError", "check_device_status",
 }
 

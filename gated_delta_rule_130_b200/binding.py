@@ -74,6 +74,25 @@ def _load():
     lib.gdn_chunk_fwd_cw_workspace_size.restype = Z
     lib.gdn_decode_step_cw.argtypes = [vp, vp, vp, fp, fp, fp, fp, vp, I, I, I, I, I, vp]
     lib.gdn_decode_step_cw.restype = I
+    L, Fl = ctypes.c_longlong, ctypes.c_float
+    lib.gdn_decode_runs.argtypes = [vp, vp, vp, fp, fp, fp, vp, vp, vp, I, I, I, I, I, I, I, L, L,
+                                    L, L, L, I, U, vp]
+    lib.gdn_decode_runs.restype = I
+    lib.gdn_short_conv_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, I, I, I, I, I, I, L, I,
+                                       I, I, vp]
+    lib.gdn_short_conv_fwd.restype = I
+    lib.gdn_short_conv_bwd.argtypes = [vp, vp, vp, I, vp, vp, vp, vp, vp, fp, fp, I, I, I, I, L, I,
+                                       I, I, vp, Z, vp]
+    lib.gdn_short_conv_bwd.restype = I
+    lib.gdn_short_conv_bwd_workspace_size.argtypes = [I, I, I]
+    lib.gdn_short_conv_bwd_workspace_size.restype = Z
+    lib.gdn_rms_norm_fwd.argtypes = [vp, vp, vp, vp, vp, fp, vp, I, I, I, I, L, L, L, Fl, I, I, vp]
+    lib.gdn_rms_norm_fwd.restype = I
+    lib.gdn_rms_norm_bwd.argtypes = [vp, vp, vp, vp, vp, vp, fp, vp, I, I, I, L, L, L, L, Fl, I, I,
+                                     vp, Z, vp]
+    lib.gdn_rms_norm_bwd.restype = I
+    lib.gdn_rms_norm_bwd_workspace_size.argtypes = [I, I, I]
+    lib.gdn_rms_norm_bwd_workspace_size.restype = Z
     lib.gdn_debug_withhold_first_arrival.argtypes = [I]
     lib.gdn_debug_withhold_first_arrival.restype = I
     lib.gdn_check_device_status.argtypes = []
@@ -451,3 +470,327 @@ def decode_step(q, k, v, log_alpha, beta, S, out=None, l2norm_qk: bool = False,
         _flags(l2norm_qk, gate_logits), _stream_ptr(dev))
     _check(st, "gdn_decode_step")
     return o
+
+
+# ---------------------------------------------------------------------------
+# The operators around the rule (gdn_decode_runs, gdn_short_conv_*, gdn_rms_norm_*).
+
+GDN_FLAG_READ_ONLY = 4
+
+
+def _rows(t: torch.Tensor, name: str, dtype, device):
+    """Pointer and token stride of [tokens, ...] whose tokens are dense."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise GdnError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise GdnError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise GdnError(f"{name} is on {t.device}, expected {device}")
+    width, shape, strides = 1, t.shape, t.stride()
+    for i in range(len(shape) - 1, 0, -1):
+        if shape[i] != 1 and strides[i] != width:
+            raise GdnError(f"{name}: the channels of a token must be contiguous")
+        width *= shape[i]
+    return t.data_ptr(), strides[0] if shape[0] > 1 else max(width, 1)
+
+
+def _param(t: torch.Tensor, name: str, shape, dtype, device):
+    if t.shape != shape:
+        raise GdnError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype != torch.float32 and t.dtype != dtype:
+        raise GdnError(f"{name} must be float32 or {dtype}, got {t.dtype}")
+    return _dev(t, name, None, device)
+
+
+def _call(device, f, *args):
+    """f(*args, stream) with ``device`` current."""
+    if device.index == torch.cuda.current_device():
+        return f(*args, _stream_ptr(device))
+    with torch.cuda.device(device):
+        return f(*args, _stream_ptr(device))
+
+
+def _scratch(need: int, workspace, device):
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    return _dev(workspace, "workspace", None, device), workspace.numel() * workspace.element_size()
+
+
+def _sequences(cu_seqlens, slots, total, device):
+    """Pointers of the offsets and slots (int32 device tensors) and the number of sequences."""
+    cu = sl = None
+    N = total
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise GdnError("cu_seqlens must hold N + 1 offsets")
+        N = cu_seqlens.numel() - 1
+        cu = _dev(cu_seqlens, "cu_seqlens", torch.int32, device)
+    if slots is not None:
+        if slots.shape != (N,):
+            raise GdnError("slots must hold one slot per sequence")
+        sl = _dev(slots, "slots", torch.int32, device)
+    return cu, sl, N
+
+
+def decode_runs(q, k, v, log_alpha, beta, states, slots=None, cu_seqlens=None, out=None,
+                update: bool = True, l2norm_qk: bool = False, gate_logits: bool = False,
+                want_output: bool = True):
+    """Runs of tokens over a pool of states; returns o [total, Hv, Dv] (None without output).
+
+    q, k [total, Hk, Dk], v [total, Hv, Dv] float32 or bfloat16 and log_alpha, beta
+    [total, Hv] float32 may be slices of wider rows; Hv is a multiple of Hk (value
+    head h reads key head h // (Hv // Hk)).  ``states`` [n_slots, Hv, Dv, Dk] float32
+    is advanced in place, sequence n (tokens cu_seqlens[n] .. cu_seqlens[n + 1] - 1;
+    None: one token each) in slot slots[n] (None: n).  ``cu_seqlens`` and ``slots`` are
+    int32 tensors on q's device.  ``update=False`` leaves the states alone (outputs of
+    a draft); ``want_output=False`` only advances them (q may be None).  A slot below 0
+    marks a row of padding: output zero, no state.  Rows of no sequence are not written:
+    they keep what ``out`` held.  ``l2norm_qk`` / ``gate_logits``: the
+    input prologue, as in ``chunk_fwd``.
+    """
+    if not want_output and out is not None:
+        raise GdnError("out without want_output")
+    if want_output and q is None:
+        raise GdnError("q is needed for the output")
+    if k.dim() != 3 or v.dim() != 3 or v.shape[0] != k.shape[0] or (q is not None and
+                                                                  q.shape != k.shape):
+        raise GdnError("q, k must be [total,Hk,Dk] and v [total,Hv,Dv]")
+    total, Hk, Dk = k.shape
+    _, Hv, Dv = v.shape
+    dev, dtype = k.device, k.dtype
+    code = _dtype_code(k)
+    if log_alpha.shape != (total, Hv) or beta.shape != (total, Hv):
+        raise GdnError("log_alpha and beta must be [total,Hv]")
+    if states.dim() != 4 or states.shape[1:] != (Hv, Dv, Dk):
+        raise GdnError("states must be [n_slots,Hv,Dv,Dk]")
+    if Hk == 0 or Hv % Hk:
+        raise GdnError("Hv must be a multiple of Hk")
+    kp, ks = _rows(k, "k", dtype, dev)
+    qp, qs = _rows(q, "q", dtype, dev) if q is not None else (None, 0)
+    vp, vs = _rows(v, "v", dtype, dev)
+    ap, as_ = _rows(log_alpha, "log_alpha", torch.float32, dev)
+    bp, bs = _rows(beta, "beta", torch.float32, dev)
+    cu, sl, N = _sequences(cu_seqlens, slots, total, dev)
+    if slots is None and N > states.shape[0]:
+        raise GdnError("without slots, states must hold one state per sequence")
+    o = op = None
+    if want_output:
+        o = out if out is not None else torch.empty((total, Hv, Dv), dtype=dtype, device=dev)
+        if o.shape != (total, Hv, Dv):
+            raise GdnError("out must be [total,Hv,Dv]")
+        op = _dev(o, "out", dtype, dev)
+    flags = _flags(l2norm_qk, gate_logits) | (0 if update else GDN_FLAG_READ_ONLY)
+    st = _call(dev, LIB.gdn_decode_runs, qp, kp, vp, ap, bp,
+               _dev(states, "states", torch.float32, dev), sl, cu, op, N, total, Hk, Hv, Dk, Dv,
+               states.shape[0], qs, ks, vs, as_, bs, code, flags)
+    _check(st, "gdn_decode_runs")
+    return o
+
+
+def _parts(tensors, splits, total, dtype, dev, name):
+    """Pointers, strides and channel offsets (ctypes arrays) of the parts of y or dy."""
+    n = len(tensors)
+    ptrs, strides = (ctypes.c_void_p * n)(), (ctypes.c_longlong * n)()
+    begin = (ctypes.c_int * (n + 1))()
+    for i, (t, c) in enumerate(zip(tensors, splits)):
+        if t.shape != (total, c):
+            raise GdnError(f"{name} must be [total,C], split as the channels are")
+        ptrs[i], strides[i] = _rows(t, name, dtype, dev)
+        begin[i + 1] = begin[i] + c
+    return ptrs, strides, begin
+
+
+def short_conv_fwd(x, weight, bias=None, cu_seqlens=None, states=None, slots=None, silu: bool = True,
+                   splits=None, out=None):
+    """Short causal depthwise convolution over packed sequences: y [total, C].
+
+    z[t] = bias + sum_j weight[:, j] * x[t - (W - 1) + j], y = silu(z) (or z).  x
+    [total, C] float32 or bfloat16, possibly a slice of wider rows; weight [C, W], W in
+    2..4, and bias [C] float32 or x's type.  ``splits``: up to three widths that sum to
+    C; y is then a tuple of arrays of these widths (q, k and v from one call).
+    ``states`` [n_slots, W - 1, C] in x's type: the last inputs of each sequence, used
+    in front of it and replaced; ``slots`` and ``cu_seqlens`` as in ``decode_runs``.
+    Without states sequences start from zero.  Rows of no sequence are not written: they
+    keep what ``out`` held.
+    """
+    if x.dim() != 2 or weight.dim() != 2:
+        raise GdnError("x must be [total,C] and weight [C,W]")
+    total, C = x.shape
+    W = weight.shape[1]
+    dev, dtype = x.device, x.dtype
+    code = _dtype_code(x)
+    xp, xs = _rows(x, "x", dtype, dev)
+    wp = _param(weight, "weight", (C, W), dtype, dev)
+    bp = None
+    if bias is not None:
+        if bias.dtype != weight.dtype:
+            raise GdnError("bias and weight must have one type")
+        bp = _param(bias, "bias", (C,), dtype, dev)
+    if slots is not None and states is None:
+        raise GdnError("slots without states")
+    cu, sl, N = _sequences(cu_seqlens, slots, total, dev)
+    sp, n_slots = None, 0
+    if states is not None:
+        if states.dim() != 3 or states.shape[1:] != (W - 1, C):
+            raise GdnError("states must be [n_slots,W-1,C]")
+        n_slots = states.shape[0]
+        if slots is None and N > n_slots:
+            raise GdnError("without slots, states must hold one state per sequence")
+        sp = _dev(states, "states", dtype, dev)
+    widths = [C] if splits is None else list(splits)
+    if not 1 <= len(widths) <= 3 or sum(widths) != C or min(widths) <= 0:
+        raise GdnError("splits must be one to three widths that sum to C")
+    if out is None:
+        ys = tuple(torch.empty((total, c), dtype=dtype, device=dev) for c in widths)
+    else:
+        ys = (out,) if splits is None else tuple(out)
+        if len(ys) != len(widths):
+            raise GdnError("out must hold one array per split")
+    ptrs, strides, begin = _parts(ys, widths, total, dtype, dev, "out")
+    st = _call(dev, LIB.gdn_short_conv_fwd, xp, wp, bp, sp, sl, cu, ptrs, strides, begin,
+               len(widths), N, total, C, W, n_slots, xs, int(silu), code, _dtype_code(weight))
+    _check(st, "gdn_short_conv_fwd")
+    return ys[0] if splits is None else ys
+
+
+def short_conv_bwd_workspace_size(total: int, C: int, W: int) -> int:
+    return int(LIB.gdn_short_conv_bwd_workspace_size(total, C, W))
+
+
+def short_conv_bwd(dy, x, weight, bias=None, cu_seqlens=None, silu: bool = True, workspace=None):
+    """Gradients of ``short_conv_fwd`` for sequences that start from zero.
+
+    ``dy`` [total, C] or a tuple of the parts' gradients; the rest as in the forward.
+    Returns (dx [total, C] in x's type, dweight [C, W] float32, dbias [C] float32 or
+    None without bias).
+    """
+    if x.dim() != 2 or weight.dim() != 2:
+        raise GdnError("x must be [total,C] and weight [C,W]")
+    total, C = x.shape
+    W = weight.shape[1]
+    dev, dtype = x.device, x.dtype
+    code = _dtype_code(x)
+    xp, xs = _rows(x, "x", dtype, dev)
+    wp = _param(weight, "weight", (C, W), dtype, dev)
+    bp = None
+    if bias is not None:
+        if bias.dtype != weight.dtype:
+            raise GdnError("bias and weight must have one type")
+        bp = _param(bias, "bias", (C,), dtype, dev)
+    cu, _, N = _sequences(cu_seqlens, None, total, dev)
+    dys = (dy,) if isinstance(dy, torch.Tensor) else tuple(dy)
+    if not 1 <= len(dys) <= 3 or any(d.dim() != 2 for d in dys) or sum(d.shape[1] for d in dys) != C:
+        raise GdnError("dy must be [total,C] or up to three arrays of C channels in all")
+    ptrs, strides, begin = _parts(dys, [d.shape[1] for d in dys], total, dtype, dev, "dy")
+    dx = torch.empty((total, C), dtype=dtype, device=dev)
+    dw = torch.empty((C, W), dtype=torch.float32, device=dev)
+    db = torch.empty((C,), dtype=torch.float32, device=dev) if bias is not None else None
+    ws, nbytes = _scratch(int(LIB.gdn_short_conv_bwd_workspace_size(total, C, W)), workspace, dev)
+    st = _call(dev, LIB.gdn_short_conv_bwd, ptrs, strides, begin, len(dys), xp, wp, bp, cu,
+               dx.data_ptr(), dw.data_ptr(), db.data_ptr() if db is not None else None, N, total,
+               C, W, xs, int(silu), code, _dtype_code(weight), ws, nbytes)
+    _check(st, "gdn_short_conv_bwd")
+    return dx, dw, db
+
+
+def _norm_rows(t, name, shape, dtype, dev):
+    """Pointer and token stride of a [..., D] tensor: its last axis but one counts the heads
+    of a token where there are three axes or more, the axes before it the tokens."""
+    if t.shape != shape:
+        raise GdnError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dim() == 1:
+        t = t.unsqueeze(0)
+    elif t.dim() > 3:
+        try:
+            t = t.view(-1, *t.shape[-2:])
+        except RuntimeError:
+            raise GdnError(f"{name}: its leading axes must be contiguous with one another") from None
+    return _rows(t, name, dtype, dev)
+
+
+def _norm_sizes(shape):
+    if len(shape) < 1 or shape[-1] < 1:
+        raise GdnError("x must be [...,D] with D >= 1")
+    heads = shape[-2] if len(shape) > 2 else 1
+    tokens = 1
+    for n in shape[:-2] if len(shape) > 2 else shape[:-1]:
+        tokens *= n
+    return tokens, heads, shape[-1]
+
+
+def rms_norm_fwd(x, weight, residual=None, gate=None, eps: float = 1e-6, quant=None, out=None,
+                 h_out=None):
+    """Root-mean-square norm over the last axis: returns (y, scale, h).
+
+    h = x + residual, rounded to x's type (h is None and x is used without residual);
+    y = h / sqrt(mean h^2 + eps) * weight (* silu(gate)).  x, residual and gate [..., D]
+    float32 or bfloat16, with three axes or more the last but one being a token's
+    heads; tokens may be slices of wider rows.  weight [D] float32 or x's type.
+    ``quant``: None: y in x's type; "row" or "group": y in float8_e4m3fn, with ``scale``
+    [..., D / group] float32 per row or per 128 columns, the value being y * scale.
+    ``out`` / ``h_out``: arrays for y and h (h_out may be the residual itself).
+    """
+    shape, dev, dtype = x.shape, x.device, x.dtype
+    code = _dtype_code(x)
+    tokens, heads, D = _norm_sizes(shape)
+    xp, xs = _norm_rows(x, "x", shape, dtype, dev)
+    wp = _param(weight, "weight", (D,), dtype, dev)
+    rp, rs = _norm_rows(residual, "residual", shape, dtype, dev) if residual is not None else (None, 0)
+    gp, gs = _norm_rows(gate, "gate", shape, dtype, dev) if gate is not None else (None, 0)
+    if quant not in (None, "row", "group"):
+        raise GdnError('quant must be None, "row" or "group"')
+    group = 0 if quant is None else D if quant == "row" else 128
+    if quant == "group" and D % 128:
+        raise GdnError("groups of 128 columns need D to be a multiple of 128")
+    ytype = dtype if quant is None else torch.float8_e4m3fn
+    y = out if out is not None else torch.empty(shape, dtype=ytype, device=dev)
+    if y.shape != shape:
+        raise GdnError("out must be shaped like x")
+    yp = _dev(y, "out", ytype, dev)
+    scale = sc = None
+    if group:
+        scale = torch.empty(shape[:-1] + (D // group,), dtype=torch.float32, device=dev)
+        sc = scale.data_ptr()
+    h = hp = None
+    if residual is not None:
+        h = h_out if h_out is not None else torch.empty(shape, dtype=dtype, device=dev)
+        if h.shape != shape:
+            raise GdnError("h_out must be shaped like x")
+        hp = _dev(h, "h_out", dtype, dev)
+    elif h_out is not None:
+        raise GdnError("h_out without residual")
+    st = _call(dev, LIB.gdn_rms_norm_fwd, xp, wp, rp, gp, yp, sc, hp, tokens, heads, D, group, xs,
+               rs, gs, eps, code, _dtype_code(weight))
+    _check(st, "gdn_rms_norm_fwd")
+    return y, scale, h
+
+
+def rms_norm_bwd_workspace_size(tokens: int, heads: int, D: int) -> int:
+    return int(LIB.gdn_rms_norm_bwd_workspace_size(tokens, heads, D))
+
+
+def rms_norm_bwd(dy, x, weight, gate=None, d_res=None, eps: float = 1e-6, workspace=None):
+    """Gradients of ``rms_norm_fwd``: returns (dx, dweight, dgate).
+
+    ``x`` is the forward's x, or its h where there was a residual; ``dy`` the gradient of
+    y (of the values it stands for, where it is held in 8 bits); ``d_res`` that of h, if
+    h is used again.  dx, in x's type, is the gradient of both x and the residual;
+    dweight [D] is float32; dgate is None without gate.
+    """
+    shape, dev, dtype = x.shape, x.device, x.dtype
+    code = _dtype_code(x)
+    tokens, heads, D = _norm_sizes(shape)
+    xp, xs = _norm_rows(x, "x", shape, dtype, dev)
+    yp, ys = _norm_rows(dy, "dy", shape, dtype, dev)
+    wp = _param(weight, "weight", (D,), dtype, dev)
+    gp, gs = _norm_rows(gate, "gate", shape, dtype, dev) if gate is not None else (None, 0)
+    dp, ds = _norm_rows(d_res, "d_res", shape, dtype, dev) if d_res is not None else (None, 0)
+    dx = torch.empty(shape, dtype=dtype, device=dev)
+    dw = torch.empty((D,), dtype=torch.float32, device=dev)
+    dgate = torch.empty(shape, dtype=dtype, device=dev) if gate is not None else None
+    ws, nbytes = _scratch(int(LIB.gdn_rms_norm_bwd_workspace_size(tokens, heads, D)), workspace, dev)
+    st = _call(dev, LIB.gdn_rms_norm_bwd, yp, xp, wp, gp, dp, dx.data_ptr(), dw.data_ptr(),
+               dgate.data_ptr() if dgate is not None else None, tokens, heads, D, ys, xs, gs, ds,
+               eps, code, _dtype_code(weight), ws, nbytes)
+    _check(st, "gdn_rms_norm_bwd")
+    return dx, dw, dgate

@@ -169,6 +169,59 @@ cudaError_t launch_chunk_cw_tc(const void *q, const void *k, const void *v, cons
                                float *S_T, int B, int T, int H, int Dv, void *workspace,
                                cudaStream_t st);
 
+// Runs of tokens over a pool of states: decode_runs.cu.  Strides are in elements
+// per token; cu == nullptr: one token per sequence; slots == nullptr: sequence n
+// has slot n; o == nullptr: only the states advance.
+struct RunsArgs {
+    const void *q, *k, *v;
+    const float *log_alpha, *beta;
+    float *states;
+    const int *slots, *cu;
+    void *o;
+    int N, total, Hk, Hv, Dk, Dv, n_slots;
+    long long q_stride, k_stride, v_stride, la_stride, be_stride;
+    unsigned flags;
+    bool update;
+};
+cudaError_t launch_decode_runs(const RunsArgs &a, bool bf16, cudaStream_t st);
+
+// Short causal depthwise convolution: short_conv.cu.  The channels of y (dy) lie
+// in up to kConvParts arrays, part p holding the channels [begin[p], begin[p + 1]).
+constexpr int kConvParts = 3;
+struct ConvArgs {
+    const void *x, *weight, *bias;
+    void *states;
+    const int *slots, *cu;
+    void *part[kConvParts];             // y of the forward, dy of the backward
+    long long part_stride[kConvParts];  // elements per token
+    int begin[kConvParts + 1];
+    void *dx;                           // backward only, as dw, db, partial
+    float *dw, *db, *partial;
+    int N, total, C, W, n_slots, parts;
+    long long x_stride;
+    bool weight_f32, silu;
+};
+cudaError_t launch_short_conv_fwd(const ConvArgs &a, bool bf16, cudaStream_t st);
+size_t short_conv_bwd_bytes(int total, int C, int W);
+cudaError_t launch_short_conv_bwd(const ConvArgs &a, bool bf16, cudaStream_t st);
+
+// Root-mean-square norm over rows of D: rms_norm.cu.  Row r is head r % H of token
+// r / H, its elements at token * stride + head * D; outputs are dense.
+struct NormArgs {
+    const void *x, *weight, *residual, *gate, *dy, *d_res;
+    void *y, *h;
+    float *scale;
+    void *dx, *dgate;                   // backward only, as dw, partial
+    float *dw, *partial;
+    int rows, H, D, group;              // group: columns per 8-bit scale, 0: y in x's type
+    long long x_stride, res_stride, gate_stride, dy_stride, dres_stride;
+    float eps;
+    bool weight_f32;
+};
+cudaError_t launch_rms_norm_fwd(const NormArgs &a, bool bf16, cudaStream_t st);
+size_t rms_norm_bwd_bytes(int rows, int D);
+cudaError_t launch_rms_norm_bwd(const NormArgs &a, bool bf16, cudaStream_t st);
+
 // Read and clear the flag a fused-kernel CTA sets when one of its bounded waits
 // times out (synchronous).
 cudaError_t read_and_clear_device_error(unsigned int *flag);

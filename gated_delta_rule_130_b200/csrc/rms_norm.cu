@@ -1,0 +1,547 @@
+// Root-mean-square norm of rows of D elements,
+//     h = x (+ residual, rounded to x's type: the residual stream is held in it),
+//     y = h rstd w (silu(gate)),   rstd = 1 / sqrt(mean h^2 + eps),
+// y in x's type or in 8 bits (e4m3) with a scale = max|y| / 448 per row or per 128
+// columns; and its gradients, with n = h rstd, dn = dy (silu(gate)):
+//     dx = rstd (w dn) - h rstd^3 mean(w dn h) (+ d_res),  dw = sum over rows of dn n,
+//     dgate = dy n w silu'(gate).
+// rstd is formed again in the backward: its sum runs beside that of w dn h.
+//
+// Both directions read and write each element once and are bound by HBM.  A row is
+// held in the registers of TPR threads (part of a warp, a warp or a block) as IT
+// vectors of 16 bytes each; sums are float32.
+#include <cuda_fp8.h>
+
+#include "kernels.h"
+#include "vec.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr float kE4M3Max = 448.f;
+constexpr float kTinyMax = 1e-30f;  // smallest maximum that a scale is made from
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
+template <int LANES, bool MAX>
+__device__ __forceinline__ float lanes_reduce(float x) {
+#pragma unroll
+    for (int off = LANES / 2; off > 0; off >>= 1) {
+        const float y = __shfl_xor_sync(0xffffffffu, x, off);
+        x = MAX ? max_nan(x, y) : x + y;
+    }
+    return x;
+}
+
+// Sum (maximum) over the TPR threads of a row; TPR above 32: over the block, by way
+// of `part` (one float per warp; the caller has a barrier between two uses).
+template <int TPR, bool MAX>
+__device__ __forceinline__ float row_reduce(float x, float *part) {
+    x = lanes_reduce<(TPR < 32 ? TPR : 32), MAX>(x);
+    if (TPR > 32) {
+        if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = x;
+        __syncthreads();
+        x = part[0];
+        for (int i = 1; i < (int)blockDim.x / 32; ++i) x = MAX ? max_nan(x, part[i]) : x + part[i];
+    }
+    return x;
+}
+
+__device__ __forceinline__ float quant_inverse(float top, float *scale) {
+    top = max_nan(top, kTinyMax);
+    *scale = top * (1.f / kE4M3Max);
+    return kE4M3Max / top;
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&x)[VEC], float inv) {
+    if constexpr (VEC == 1) {
+        *p = __nv_cvt_float_to_fp8(x[0] * inv, __NV_SATFINITE, __NV_E4M3);
+    } else {
+        uint32_t w[VEC / 4];
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+                make_float2(x[4 * i] * inv, x[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+                make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+            w[i] = lo | (hi << 16);
+        }
+        if constexpr (VEC == 8)
+            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        else
+            *reinterpret_cast<uint32_t *>(p) = w[0];
+    }
+}
+
+// Element offset of row r in a tensor with `stride` elements per token.
+__device__ __forceinline__ long long row_at(const NormArgs &a, int r, long long stride) {
+    return (long long)(r / a.H) * stride + (long long)(r % a.H) * a.D;
+}
+
+// A row in registers: D <= VEC * TPR * IT, D a multiple of VEC.
+template <typename T, int VEC, int TPR, int IT>
+__global__ void __launch_bounds__(TPR > 32 ? TPR : 256)
+rms_fwd(NormArgs a) {
+    constexpr int RPB = TPR > 32 ? 1 : 256 / TPR;  // rows per block
+    __shared__ float part[2][32];
+    const int sub = threadIdx.x % TPR;
+    const int r = blockIdx.x * RPB + threadIdx.x / TPR;
+    const bool live = r < a.rows;
+    const int row = live ? r : 0;
+    const T *x = static_cast<const T *>(a.x) + row_at(a, row, a.x_stride);
+    const T *res = a.residual ? static_cast<const T *>(a.residual) + row_at(a, row, a.res_stride)
+                              : nullptr;
+    const T *gate = a.gate ? static_cast<const T *>(a.gate) + row_at(a, row, a.gate_stride) : nullptr;
+    const long long out = (long long)row * a.D;
+
+    float h[IT][VEC];
+    Raw<T, VEC> g[IT];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int c = (i * TPR + sub) * VEC;
+        if (live && c < a.D) {
+            load_vec<T, VEC>(x + c, h[i]);
+            if (res) {
+                float b[VEC];
+                load_vec<T, VEC>(res + c, b);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) h[i][e] = to_f32(from_f32<T>(h[i][e] + b[e]));
+            }
+            if (gate) g[i] = load_raw<T, VEC>(gate + c);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) h[i][e] = 0.f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int c = (i * TPR + sub) * VEC;
+        if (a.h && live && c < a.D) store_vec(static_cast<T *>(a.h) + out + c, h[i]);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) ss += h[i][e] * h[i][e];
+    }
+    const float rstd = rsqrtf(row_reduce<TPR, false>(ss, part[0]) / a.D + a.eps);
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int c = (i * TPR + sub) * VEC;
+        if (live && c < a.D) {
+            float w[VEC];
+            load_param<T, VEC>(a.weight, c, a.weight_f32, w);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) h[i][e] *= rstd * w[e];
+            if (gate) {
+                float gg[VEC];
+                widen(g[i], gg);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) h[i][e] *= gg[e] * fast_sigmoid(gg[e]);
+            }
+            if (!a.group) store_vec(static_cast<T *>(a.y) + out + c, h[i]);
+        }
+        if (a.group) {
+            float t = 0.f;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) t = max_nan(t, fabsf(h[i][e]));
+            if (a.group == a.D) {
+                top = max_nan(top, t);
+            } else {  // 128 columns: 128 / VEC neighbouring lanes (TPR is no smaller)
+                constexpr int LANES = 128 / VEC < TPR ? 128 / VEC : TPR;
+                float scale;
+                const float inv = quant_inverse(lanes_reduce<(LANES < 32 ? LANES : 32), true>(t), &scale);
+                if (live && c < a.D) {
+                    store_e4m3<VEC>(static_cast<uint8_t *>(a.y) + out + c, h[i], inv);
+                    if (c % 128 == 0) a.scale[(out + c) / 128] = scale;
+                }
+            }
+        }
+    }
+    if (a.group && a.group == a.D) {
+        float scale;
+        const float inv = quant_inverse(row_reduce<TPR, true>(top, part[1]), &scale);
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int c = (i * TPR + sub) * VEC;
+            if (live && c < a.D) {
+                store_e4m3<VEC>(static_cast<uint8_t *>(a.y) + out + c, h[i], inv);
+                if (c == 0) a.scale[row] = scale;
+            }
+        }
+    }
+}
+
+constexpr int kAnyThreads = 256;
+
+// Any D and any alignment: a block per row, element by element, reading again what
+// does not fit in registers.
+template <typename T>
+__global__ void __launch_bounds__(kAnyThreads)
+rms_fwd_any(NormArgs a) {
+    __shared__ float part[2][32];
+    const int row = blockIdx.x;
+    const T *x = static_cast<const T *>(a.x) + row_at(a, row, a.x_stride);
+    const T *res = a.residual ? static_cast<const T *>(a.residual) + row_at(a, row, a.res_stride)
+                              : nullptr;
+    const T *gate = a.gate ? static_cast<const T *>(a.gate) + row_at(a, row, a.gate_stride) : nullptr;
+    const long long out = (long long)row * a.D;
+    // h may take the place of x or of the residual, y that of x: once a.h is
+    // written, h is read from there
+    float ss = 0.f;
+    for (int c = threadIdx.x; c < a.D; c += kAnyThreads) {
+        float h = to_f32(x[c]);
+        if (res) h = to_f32(from_f32<T>(h + to_f32(res[c])));
+        if (a.h) static_cast<T *>(a.h)[out + c] = from_f32<T>(h);
+        ss += h * h;
+    }
+    const float rstd = rsqrtf(row_reduce<kAnyThreads, false>(ss, part[0]) / a.D + a.eps);
+    const T *hp = a.h ? static_cast<const T *>(a.h) + out : x;
+    auto value = [&](int c) {
+        float w[1];
+        load_param<T, 1>(a.weight, c, a.weight_f32, w);
+        float y = to_f32(hp[c]) * (rstd * w[0]);
+        if (gate) {
+            const float g = to_f32(gate[c]);
+            y *= g * fast_sigmoid(g);
+        }
+        return y;
+    };
+    if (!a.group) {
+        for (int c = threadIdx.x; c < a.D; c += kAnyThreads)
+            static_cast<T *>(a.y)[out + c] = from_f32<T>(value(c));
+        return;
+    }
+    uint8_t *y = static_cast<uint8_t *>(a.y) + out;
+    if (a.group == a.D) {
+        float top = 0.f, scale;
+        for (int c = threadIdx.x; c < a.D; c += kAnyThreads) top = max_nan(top, fabsf(value(c)));
+        const float inv = quant_inverse(row_reduce<kAnyThreads, true>(top, part[1]), &scale);
+        for (int c = threadIdx.x; c < a.D; c += kAnyThreads) {
+            const float v[1] = {value(c)};
+            store_e4m3<1>(y + c, v, inv);
+        }
+        if (threadIdx.x == 0) a.scale[row] = scale;
+        return;
+    }
+    const int lane = threadIdx.x % 32;
+    for (int c0 = threadIdx.x / 32 * 128; c0 < a.D; c0 += kAnyThreads / 32 * 128) {
+        float v[4][1], top = 0.f, scale;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i][0] = value(c0 + lane + 32 * i);  // D is a multiple of 128 here
+            top = max_nan(top, fabsf(v[i][0]));
+        }
+        const float inv = quant_inverse(lanes_reduce<32, true>(top), &scale);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store_e4m3<1>(y + c0 + lane + 32 * i, v[i], inv);
+        if (lane == 0) a.scale[(out + c0) / 128] = scale;
+    }
+}
+
+// Backward, a row in registers; each block takes the rows blockIdx.x * RPB + ... in
+// steps of the grid, keeps its columns' sums for dw in registers and leaves them in
+// partial[blockIdx.x].
+template <typename T, int VEC, int TPR, int IT>
+__global__ void __launch_bounds__(TPR > 32 ? TPR : 256)
+rms_bwd(NormArgs a) {
+    constexpr int RPB = TPR > 32 ? 1 : 256 / TPR;
+    __shared__ float part[2][32][2];
+    __shared__ float cols[TPR > 32 ? 1 : VEC * TPR * IT];
+    const int sub = threadIdx.x % TPR;
+    float dw[IT][VEC];
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) dw[i][e] = 0.f;
+    int turn = 0;
+    for (int r0 = blockIdx.x * RPB; r0 < a.rows; r0 += gridDim.x * RPB, turn ^= 1) {
+        const int r = r0 + threadIdx.x / TPR;
+        const bool live = r < a.rows;
+        const int row = live ? r : 0;
+        const T *x = static_cast<const T *>(a.x) + row_at(a, row, a.x_stride);
+        const T *dy = static_cast<const T *>(a.dy) + row_at(a, row, a.dy_stride);
+        const T *gate = a.gate ? static_cast<const T *>(a.gate) + row_at(a, row, a.gate_stride)
+                               : nullptr;
+        const T *dres = a.d_res ? static_cast<const T *>(a.d_res) + row_at(a, row, a.dres_stride)
+                                : nullptr;
+        const long long out = (long long)row * a.D;
+        float h[IT][VEC], d[IT][VEC];  // d: dn
+        Raw<T, VEC> g[IT], dr[IT];
+        float ss = 0.f, sd = 0.f;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int c = (i * TPR + sub) * VEC;
+            if (live && c < a.D) {
+                load_vec<T, VEC>(x + c, h[i]);
+                load_vec<T, VEC>(dy + c, d[i]);
+                if (gate) g[i] = load_raw<T, VEC>(gate + c);
+                if (dres) dr[i] = load_raw<T, VEC>(dres + c);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) h[i][e] = d[i][e] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int c = (i * TPR + sub) * VEC;
+            if (live && c < a.D) {
+                float w[VEC];
+                load_param<T, VEC>(a.weight, c, a.weight_f32, w);
+                float gg[VEC];
+                if (gate) widen(g[i], gg);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float dn = gate ? d[i][e] * (gg[e] * fast_sigmoid(gg[e])) : d[i][e];
+                    ss += h[i][e] * h[i][e];
+                    sd += w[e] * dn * h[i][e];
+                }
+            }
+        }
+        if (TPR <= 32) {
+            ss = lanes_reduce<(TPR < 32 ? TPR : 32), false>(ss);
+            sd = lanes_reduce<(TPR < 32 ? TPR : 32), false>(sd);
+        } else {
+            ss = lanes_reduce<32, false>(ss);
+            sd = lanes_reduce<32, false>(sd);
+            if (threadIdx.x % 32 == 0) {
+                part[turn][threadIdx.x / 32][0] = ss;
+                part[turn][threadIdx.x / 32][1] = sd;
+            }
+            __syncthreads();  // two rows' parts in turn: one barrier per row is enough
+            ss = sd = 0.f;
+            for (int i = 0; i < (int)blockDim.x / 32; ++i) {
+                ss += part[turn][i][0];
+                sd += part[turn][i][1];
+            }
+        }
+        const float rstd = rsqrtf(ss / a.D + a.eps);
+        const float back = sd / a.D * rstd * rstd * rstd;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int c = (i * TPR + sub) * VEC;
+            if (live && c < a.D) {
+                float w[VEC], gg[VEC], dx[VEC];
+                load_param<T, VEC>(a.weight, c, a.weight_f32, w);
+                if (gate) {
+                    widen(g[i], gg);
+                    float dg[VEC];
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float sig = fast_sigmoid(gg[e]);
+                        dg[e] = d[i][e] * (h[i][e] * rstd) * w[e] * sig * (1.f + gg[e] * (1.f - sig));
+                        d[i][e] *= gg[e] * sig;
+                    }
+                    store_vec(static_cast<T *>(a.dgate) + out + c, dg);
+                }
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    dx[e] = rstd * (w[e] * d[i][e]) - h[i][e] * back;
+                    dw[i][e] += d[i][e] * (h[i][e] * rstd);
+                }
+                if (dres) {
+                    float b[VEC];
+                    widen(dr[i], b);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) dx[e] += b[e];
+                }
+                store_vec(static_cast<T *>(a.dx) + out + c, dx);
+            }
+        }
+    }
+    float *mine = a.partial + (long long)blockIdx.x * a.D;
+    if (TPR > 32) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int c = (i * TPR + sub) * VEC;
+            if (c < a.D)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) mine[c + e] = dw[i][e];
+        }
+    } else {  // the block's row groups one after another, so that the sum has one order
+        for (int k = 0; k < RPB; ++k) {
+            if ((int)threadIdx.x / TPR == k)
+#pragma unroll
+                for (int i = 0; i < IT; ++i) {
+                    const int c = (i * TPR + sub) * VEC;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) cols[c + e] = dw[i][e] + (k ? cols[c + e] : 0.f);
+                }
+            __syncthreads();
+        }
+        for (int c = threadIdx.x; c < a.D; c += blockDim.x) mine[c] = cols[c];
+    }
+}
+
+// Backward for any D and alignment; the sums for dw of a block's rows go straight to
+// partial[blockIdx.x], each column always by the same thread.
+template <typename T>
+__global__ void __launch_bounds__(kAnyThreads)
+rms_bwd_any(NormArgs a) {
+    __shared__ float part[2][32];
+    float *mine = a.partial + (long long)blockIdx.x * a.D;
+    for (int c = threadIdx.x; c < a.D; c += kAnyThreads) mine[c] = 0.f;
+    for (int row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const T *x = static_cast<const T *>(a.x) + row_at(a, row, a.x_stride);
+        const T *dy = static_cast<const T *>(a.dy) + row_at(a, row, a.dy_stride);
+        const T *gate = a.gate ? static_cast<const T *>(a.gate) + row_at(a, row, a.gate_stride)
+                               : nullptr;
+        const T *dres = a.d_res ? static_cast<const T *>(a.d_res) + row_at(a, row, a.dres_stride)
+                                : nullptr;
+        const long long out = (long long)row * a.D;
+        float ss = 0.f, sd = 0.f, w[1];
+        for (int c = threadIdx.x; c < a.D; c += kAnyThreads) {
+            const float h = to_f32(x[c]);
+            float dn = to_f32(dy[c]);
+            if (gate) {
+                const float g = to_f32(gate[c]);
+                dn *= g * fast_sigmoid(g);
+            }
+            load_param<T, 1>(a.weight, c, a.weight_f32, w);
+            ss += h * h;
+            sd += w[0] * dn * h;
+        }
+        ss = row_reduce<kAnyThreads, false>(ss, part[0]);
+        sd = row_reduce<kAnyThreads, false>(sd, part[1]);
+        const float rstd = rsqrtf(ss / a.D + a.eps);
+        const float back = sd / a.D * rstd * rstd * rstd;
+        for (int c = threadIdx.x; c < a.D; c += kAnyThreads) {
+            const float h = to_f32(x[c]);
+            float dn = to_f32(dy[c]);
+            load_param<T, 1>(a.weight, c, a.weight_f32, w);
+            if (gate) {
+                const float g = to_f32(gate[c]), sig = fast_sigmoid(g);
+                static_cast<T *>(a.dgate)[out + c] =
+                    from_f32<T>(dn * (h * rstd) * w[0] * sig * (1.f + g * (1.f - sig)));
+                dn *= g * sig;
+            }
+            float dx = rstd * (w[0] * dn) - h * back;
+            if (dres) dx += to_f32(dres[c]);
+            static_cast<T *>(a.dx)[out + c] = from_f32<T>(dx);
+            mine[c] += dn * (h * rstd);
+        }
+        __syncthreads();  // `part` is written again
+    }
+}
+
+// dw[c] = sum over the blocks' partial sums, always in the same order.
+__global__ void __launch_bounds__(1024)
+rms_bwd_sum(const float *partial, float *dw, int blocks, int D) {
+    __shared__ float part[32][33];
+    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32, c = blockIdx.x * 32 + tx;
+    float s = 0.f;
+    if (c < D)
+        for (int b = ty; b < blocks; b += 32) s += partial[(long long)b * D + c];
+    part[ty][tx] = s;
+    __syncthreads();
+    s = lanes_reduce<32, false>(part[tx][ty]);
+    if (tx == 0 && blockIdx.x * 32 + ty < D) dw[blockIdx.x * 32 + ty] = s;
+}
+
+// Backward blocks: enough to fill 148 SMs a few times over.
+int bwd_blocks(int rows) { return rows < 592 ? rows : 592; }
+
+bool aligned(const void *p, long long stride, int elem) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * elem % 16 == 0;
+}
+bool vectors_fit(const NormArgs &a, int elem) {
+    return (long long)a.D * elem % 16 == 0 && aligned(a.x, a.x_stride, elem) &&
+           aligned(a.residual, a.res_stride, elem) && aligned(a.gate, a.gate_stride, elem) &&
+           aligned(a.dy, a.dy_stride, elem) && aligned(a.d_res, a.dres_stride, elem);
+}
+
+template <typename T, int VEC, int TPR, int IT>
+void run_fwd(const NormArgs &a, cudaStream_t st) {
+    constexpr int rpb = TPR > 32 ? 1 : 256 / TPR, threads = TPR > 32 ? TPR : 256;
+    rms_fwd<T, VEC, TPR, IT><<<(a.rows + rpb - 1) / rpb, threads, 0, st>>>(a);
+}
+template <typename T, int VEC, int TPR, int IT>
+void run_bwd(const NormArgs &a, cudaStream_t st) {
+    constexpr int rpb = TPR > 32 ? 1 : 256 / TPR, threads = TPR > 32 ? TPR : 256;
+    const int need = (a.rows + rpb - 1) / rpb, most = bwd_blocks(a.rows);
+    const int blocks = need < most ? need : most;
+    rms_bwd<T, VEC, TPR, IT><<<blocks, threads, 0, st>>>(a);
+    rms_bwd_sum<<<(a.D + 31) / 32, 1024, 0, st>>>(a.partial, a.dw, blocks, a.D);
+}
+
+template <typename T, int VEC>
+cudaError_t fwd_t(const NormArgs &a, cudaStream_t st) {
+    const int nv = a.D / VEC;  // vectors per row
+    if (!vectors_fit(a, sizeof(T)) || nv > 4096) {
+        rms_fwd_any<T><<<a.rows, kAnyThreads, 0, st>>>(a);
+    } else if (nv <= 4) {
+        run_fwd<T, VEC, 4, 1>(a, st);
+    } else if (nv <= 8) {
+        run_fwd<T, VEC, 8, 1>(a, st);
+    } else if (nv <= 16) {
+        run_fwd<T, VEC, 16, 1>(a, st);
+    } else if (nv <= 32) {
+        run_fwd<T, VEC, 32, 1>(a, st);
+    } else if (nv <= 64) {
+        run_fwd<T, VEC, 32, 2>(a, st);
+    } else if (nv <= 128) {
+        run_fwd<T, VEC, 32, 4>(a, st);
+    } else if (nv <= 256) {
+        run_fwd<T, VEC, 128, 2>(a, st);
+    } else if (nv <= 512) {
+        run_fwd<T, VEC, 256, 2>(a, st);
+    } else if (nv <= 1024) {
+        run_fwd<T, VEC, 512, 2>(a, st);
+    } else if (nv <= 2048) {
+        run_fwd<T, VEC, 1024, 2>(a, st);
+    } else {
+        run_fwd<T, VEC, 1024, 4>(a, st);
+    }
+    return cudaPeekAtLastError();
+}
+
+template <typename T, int VEC>
+cudaError_t bwd_t(const NormArgs &a, cudaStream_t st) {
+    const int nv = a.D / VEC;
+    if (!vectors_fit(a, sizeof(T)) || nv > 2048) {
+        const int blocks = bwd_blocks(a.rows);
+        rms_bwd_any<T><<<blocks, kAnyThreads, 0, st>>>(a);
+        rms_bwd_sum<<<(a.D + 31) / 32, 1024, 0, st>>>(a.partial, a.dw, blocks, a.D);
+    } else if (nv <= 4) {
+        run_bwd<T, VEC, 4, 1>(a, st);
+    } else if (nv <= 8) {
+        run_bwd<T, VEC, 8, 1>(a, st);
+    } else if (nv <= 16) {
+        run_bwd<T, VEC, 16, 1>(a, st);
+    } else if (nv <= 32) {
+        run_bwd<T, VEC, 32, 1>(a, st);
+    } else if (nv <= 64) {
+        run_bwd<T, VEC, 32, 2>(a, st);
+    } else if (nv <= 128) {
+        run_bwd<T, VEC, 128, 1>(a, st);
+    } else if (nv <= 256) {
+        run_bwd<T, VEC, 128, 2>(a, st);
+    } else if (nv <= 512) {
+        run_bwd<T, VEC, 256, 2>(a, st);
+    } else if (nv <= 1024) {
+        run_bwd<T, VEC, 512, 2>(a, st);
+    } else {
+        run_bwd<T, VEC, 1024, 2>(a, st);
+    }
+    return cudaPeekAtLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_rms_norm_fwd(const NormArgs &a, bool bf16, cudaStream_t st) {
+    return bf16 ? fwd_t<__nv_bfloat16, 8>(a, st) : fwd_t<float, 4>(a, st);
+}
+
+size_t rms_norm_bwd_bytes(int rows, int D) {
+    return (size_t)bwd_blocks(rows) * D * sizeof(float);
+}
+
+cudaError_t launch_rms_norm_bwd(const NormArgs &a, bool bf16, cudaStream_t st) {
+    return bf16 ? bwd_t<__nv_bfloat16, 8>(a, st) : bwd_t<float, 4>(a, st);
+}
+
+}  // namespace gdn

@@ -1,0 +1,73 @@
+// Vectors of consecutive elements widened to float32: VEC = 16 bytes' worth (8
+// bf16, 4 float32), or 1 where an address is not a multiple of 16 bytes.
+#pragma once
+
+#include "common.cuh"
+
+namespace gdn {
+
+template <typename T, int VEC> struct Raw;  // what one load brings
+template <> struct Raw<float, 4> { float4 r; };
+template <> struct Raw<__nv_bfloat16, 8> { uint4 r; };
+template <> struct Raw<float, 1> { float r; };
+template <> struct Raw<__nv_bfloat16, 1> { __nv_bfloat16 r; };
+
+template <typename T, int VEC>
+__device__ __forceinline__ Raw<T, VEC> load_raw(const T *p) {
+    return *reinterpret_cast<const Raw<T, VEC> *>(p);
+}
+
+__device__ __forceinline__ void widen(const Raw<float, 4> &v, float (&x)[4]) {
+    x[0] = v.r.x; x[1] = v.r.y; x[2] = v.r.z; x[3] = v.r.w;
+}
+__device__ __forceinline__ void widen(const Raw<__nv_bfloat16, 8> &v, float (&x)[8]) {
+    const uint32_t w[4] = {v.r.x, v.r.y, v.r.z, v.r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // bf16 is the upper half of a float32
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void widen(const Raw<float, 1> &v, float (&x)[1]) { x[0] = v.r; }
+__device__ __forceinline__ void widen(const Raw<__nv_bfloat16, 1> &v, float (&x)[1]) {
+    x[0] = __bfloat162float(v.r);
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void load_vec(const T *p, float (&x)[VEC]) {
+    widen(load_raw<T, VEC>(p), x);
+}
+
+__device__ __forceinline__ void store_vec(float *p, const float (&x)[4]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename T>
+__device__ __forceinline__ void store_vec(T *p, const float (&x)[1]) { *p = from_f32<T>(x[0]); }
+
+// A parameter (weight, bias) held in float32 or in T.
+template <typename T, int VEC>
+__device__ __forceinline__ void load_param(const void *p, long long at, bool f32, float (&x)[VEC]) {
+    if (f32) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) x[i] = static_cast<const float *>(p)[at + i];
+    } else {
+        load_vec<T, VEC>(static_cast<const T *>(p) + at, x);
+    }
+}
+
+// 1 / (1 + e^-x) by the fast exponential and reciprocal: off by at most a few
+// float32 roundings (1e-6 relative for |x| up to 10); 0 where e^-x overflows.
+__device__ __forceinline__ float fast_sigmoid(float x) {
+    return __fdividef(1.f, 1.f + __expf(-x));
+}
+
+}  // namespace gdn

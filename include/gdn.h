@@ -332,6 +332,130 @@ gdn_status_t gdn_decode_step_cw(const void *q, const void *k, const void *v,
                                 gdn_dtype_t dtype, void *stream);
 
 /*
+ * The operators around the rule.  A layer's q, k and v come out of a short causal
+ * convolution, its input out of a root-mean-square norm, its output goes through a
+ * gated one; in serving the states live in a pool.  Conventions as above, and:
+ *  - `..._stride` arguments count elements from one token to the next, so that an
+ *    input may be a slice of a wider projection's rows; the channels of a token are
+ *    contiguous.  Strides are at least the width of a token's row, at most 2^30 (above:
+ *    GDN_ERR_INVALID_ARG).  The gates of
+ *    gdn_decode_runs need 4-byte alignment only.  Fast paths want rows that start on
+ *    16-byte boundaries; others run element by element.
+ *  - Offsets and slots are DEVICE arrays of int32, read by the kernels alone, so a
+ *    captured graph can be replayed with others.  The kernels check them: a sequence
+ *    whose offsets are none (negative, decreasing, behind `total`) is left out; one
+ *    whose slot is not in [0, n_slots) is a row of padding: its outputs are zero
+ *    and no state is touched.  So is, where states are written, a sequence with
+ *    tokens whose slot an earlier sequence with tokens has.  Output rows that
+ *    belong to no sequence keep what they held.
+ */
+
+/*
+ * Runs of tokens over a pool of states (serving: a decode batch, drafts to be
+ * verified, the tails of prompts).  Sequence n is the tokens cu_seqlens[n] ..
+ * cu_seqlens[n + 1] - 1 and advances its state, states[slots[n]], by the rule of
+ * gdn_decode_step token by token; any length is allowed, runs up to 8 tokens are
+ * taken in one pass over the state.  Value head h reads key head h / (Hv / Hk).
+ *
+ *   q, k [total, Hk, Dk], v [total, Hv, Dv], log_alpha, beta [total, Hv] float32,
+ *   with token strides; states [n_slots, Hv, Dv, Dk] float32; o [total, Hv, Dv].
+ *   slots      : N slots, or NULL: sequence n has slot n.
+ *   cu_seqlens : N + 1 offsets, or NULL: N = total sequences of one token.
+ *   o          : NULL if only the states are wanted (q may then be NULL too).
+ *   flags      : gdn_flag_t bits and GDN_FLAG_READ_ONLY: the states are read and
+ *                not written (a draft's outputs before it is accepted; several
+ *                sequences may then share a slot).
+ * Limits: those of gdn_decode_step, Hv a multiple of Hk, N <= 65535,
+ * N * Hv * Dv < 2^31, n_slots * Hv <= 2^40.  o and states overlap nothing else.
+ */
+#define GDN_FLAG_READ_ONLY 4u
+gdn_status_t gdn_decode_runs(const void *q, const void *k, const void *v,
+                             const float *log_alpha, const float *beta, float *states,
+                             const int *slots, const int *cu_seqlens, void *o, int N, int total,
+                             int Hk, int Hv, int Dk, int Dv, int n_slots, long long q_stride,
+                             long long k_stride, long long v_stride, long long log_alpha_stride,
+                             long long beta_stride, gdn_dtype_t dtype, unsigned flags,
+                             void *stream);
+
+/*
+ * Short causal depthwise convolution over packed sequences, W in 2..4 taps:
+ *   z[t, c] = bias[c] + sum_j weight[c, j] x[t - (W - 1) + j, c],  y = silu(z) or z.
+ *
+ *   x [total, C] with a token stride; weight [C, W] and bias [C] (or NULL) in
+ *   `param_dtype` (float32 or `dtype`).
+ *   y       : `parts` (1..3) arrays, array p with the channels part_begin[p] ..
+ *             part_begin[p + 1] - 1 (HOST arrays; part_begin[0] = 0, the last C) and
+ *             part_strides[p] elements per token: q, k and v from one call.
+ *   states  : [n_slots, W - 1, C] in `dtype`, the last W - 1 inputs of each sequence,
+ *             read before its first token and replaced by its own last ones; or NULL:
+ *             sequences start from zero and slots is not looked at.
+ *   slots, cu_seqlens : as for gdn_decode_runs.
+ *   silu    : nonzero: y = silu(z).
+ * No y may overlap another argument (column slices of one array are apart).  Limits:
+ * N <= 65535, C <= 2^24, ceil(C / 128) * total < 2^31.
+ */
+gdn_status_t gdn_short_conv_fwd(const void *x, const void *weight, const void *bias, void *states,
+                                const int *slots, const int *cu_seqlens, void *const *y,
+                                const long long *part_strides, const int *part_begin, int parts,
+                                int N, int total, int C, int W, int n_slots, long long x_stride,
+                                int silu, gdn_dtype_t dtype, gdn_dtype_t param_dtype,
+                                void *stream);
+
+/*
+ * Its gradients, for sequences that start from zero: dy in the parts of y; dx
+ * [total, C] dense in `dtype` (zero for tokens of no sequence), dweight [C, W] and
+ * dbias [C] (or NULL) float32.  bias as in the forward.  The sums for dweight and
+ * dbias have one order: equal calls give equal bits.  Workspace:
+ * gdn_short_conv_bwd_workspace_size(...) bytes.
+ */
+gdn_status_t gdn_short_conv_bwd(const void *const *dy, const long long *part_strides,
+                                const int *part_begin, int parts, const void *x,
+                                const void *weight, const void *bias, const int *cu_seqlens,
+                                void *dx, float *dweight, float *dbias, int N, int total, int C,
+                                int W, long long x_stride, int silu, gdn_dtype_t dtype,
+                                gdn_dtype_t param_dtype, void *workspace, size_t workspace_bytes,
+                                void *stream);
+size_t gdn_short_conv_bwd_workspace_size(int total, int C, int W);
+
+/*
+ * Root-mean-square norm of rows of D, `heads` rows per token:
+ *   h = x + residual (rounded to `dtype`, in which the residual stream is held) or x,
+ *   y = h / sqrt(mean h^2 + eps) * weight (* silu(gate)).
+ *
+ *   x, residual, gate [tokens, heads, D] with token strides (residual, gate or
+ *   NULL); weight [D] in `param_dtype`; h_out [tokens, heads, D] dense (NULL:
+ *   not wanted; may be x or the residual itself where those are dense).
+ *   y       : [tokens, heads, D] dense: `dtype` where quant_group = 0 (may be x
+ *             itself); else e4m3 bytes with y = value * scale, one scale per
+ *             quant_group columns, which is D (a row) or 128 (D a multiple of it):
+ *             scale = max|y| / 448 of the group, float32 [rows, D / quant_group]
+ *             (groups whose largest magnitude is below 1e-30: 1e-30 / 448).  A NaN
+ *             or an infinity in a group of y makes its scale and values NaN.
+ * Limits: 1 <= D <= 2^20, tokens * heads < 2^31.
+ */
+gdn_status_t gdn_rms_norm_fwd(const void *x, const void *weight, const void *residual,
+                              const void *gate, void *y, float *scale, void *h_out, int tokens,
+                              int heads, int D, int quant_group, long long x_stride,
+                              long long residual_stride, long long gate_stride, float eps,
+                              gdn_dtype_t dtype, gdn_dtype_t param_dtype, void *stream);
+
+/*
+ * Its gradients, from dy = dL/dy [tokens, heads, D] (for an 8-bit y: of the value it
+ * stands for) and x, which is h_out where there was a residual: dx (the gradient of
+ * both x and the residual) and dgate [tokens, heads, D] dense in `dtype`, dweight
+ * [D] float32.  d_res (or NULL), dL/dh_out, is added to dx.  dgate is required with
+ * gate and NULL without.  The sums for dweight have one order: equal calls give
+ * equal bits.  Workspace: gdn_rms_norm_bwd_workspace_size(...) bytes.
+ */
+gdn_status_t gdn_rms_norm_bwd(const void *dy, const void *x, const void *weight, const void *gate,
+                              const void *d_res, void *dx, float *dweight, void *dgate, int tokens,
+                              int heads, int D, long long dy_stride, long long x_stride,
+                              long long gate_stride, long long d_res_stride, float eps,
+                              gdn_dtype_t dtype, gdn_dtype_t param_dtype, void *workspace,
+                              size_t workspace_bytes, void *stream);
+size_t gdn_rms_norm_bwd_workspace_size(int tokens, int heads, int D);
+
+/*
  * Synchronise the current device and report whether a fused tensor-core
  * kernel gave up since the last check: its pipeline waits are bounded (about
  * two seconds each); a CTA that times out stops, records a flag and leaves its
