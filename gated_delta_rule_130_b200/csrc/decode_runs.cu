@@ -9,15 +9,17 @@
 //     u_i = beta_i (v_i - gamma_i a_i - sum_{j<i} Gamma_ij (k_i.k_j) u_j)
 //     o_i = gamma_i b_i + sum_{j<=i} Gamma_ij (q_i.k_j) u_j
 //     S_r <- gamma_m S_r + sum_j Gamma_mj u_j k_j
-// which is the token recurrence S_t = alpha_t S_{t-1} + u_t k_t^T unrolled, so a
-// row costs 3 multiply-adds per element and token (2 where the state is not
-// written back) and its sums over the key channels of several tokens do not wait
-// for one another.  The Gammas are products of the decays, never quotients, so a
-// decay of 0 (log alpha = -inf) is exact.
+// which is the token recurrence S_t = alpha_t S_{t-1} + u_t k_t^T unrolled.  With
+// A_ij = beta_i Gamma_ij k_i.k_j (j < i), T = (I + A)^-1 diag(beta), P_ij = Gamma_ij
+// q_i.k_j (j <= i), M = P T and r = v - gamma a, that is u = T r and o = gamma b + M r:
+// T and M are one 8 x 8 matrix each for all rows of a head, so a row costs 3
+// multiply-adds per element and token (2 where the state is not written back) and
+// no row waits for one token after the other.  The Gammas are products of the decays,
+// never quotients, so a decay of 0 (log alpha = -inf) is exact.
 //
-// A warp holds 8 rows (4 for Dk > 128) in registers, LW lanes per row with V
-// float4 each; k and q stand in shared memory as float32, already normalised.
-// Everything is float32: the state is carried over thousands of steps.
+// A warp holds its rows in registers, LW lanes per row with V float4 each; k and q
+// stand in shared memory as float32, already normalised.  Everything is float32: the
+// state is carried over thousands of steps.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -83,36 +85,34 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
+// LW lanes share a row, V float4 each; R rows per lane group, so ROWS rows per warp.
+constexpr int R = 4;
+template <int LW> constexpr int kRows = R * (32 / LW);
+
 template <typename T, int LW, int V, bool VEC>
-__global__ void __launch_bounds__(32 * kMaxWarps)
+__global__ void __launch_bounds__(32 * kMaxWarps, 3)
 decode_runs_kernel(RunsArgs a, int row_blocks) {
-    constexpr int R = V == 1 ? 8 : 4;   // rows per lane group
-    constexpr int G = 32 / LW;          // lane groups per warp
-    constexpr int ROWS = R * G;         // rows per warp
-    constexpr int PD = LW * V * 4;      // padded Dk
-    __shared__ __align__(16) float sk[kTok][PD], sq[kTok][PD];
-    __shared__ float kk[kTok][kTok], qk[kTok][kTok];        // i >= j
+    constexpr int ROWS = kRows<LW>;
+    constexpr int PD = LW * V * 4;       // padded Dk
+    constexpr int E = (PD + 31) / 32;    // a lane's elements of k where a warp holds a token
+    __shared__ __align__(16) float sk[kTok][PD], sq[kTok][PD], sv[kTok][kMaxWarps * ROWS];
+    // tm[0]: T with u = T r, tm[1]: M with o = gamma b + M r  (r = v - gamma a)
+    __shared__ float sA[kTok][kTok], sP[kTok][kTok], tm[2][kTok][kTok];
     __shared__ float al[kTok], be[kTok], gam[kTok], tail[kTok];
-    __shared__ float da[kMaxWarps][kTok][ROWS], db[kMaxWarps][kTok][ROWS];
+    __shared__ __align__(16) float ra[kMaxWarps][ROWS][kTok], rb_[kMaxWarps][ROWS][kTok];
+    __shared__ __align__(16) float su[kMaxWarps][kTok][ROWS];
 
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, warps = blockDim.x / 32;
     const int rb = blockIdx.x % row_blocks;
     const int nh = blockIdx.x / row_blocks;
     const int n = nh / a.Hv, h = nh % a.Hv;
     const int t0 = a.cu ? a.cu[n] : n, t1 = a.cu ? a.cu[n + 1] : n + 1;
-    if (t0 < 0 || t1 > a.total || t0 >= t1) return;  // empty, or offsets that are none
     const int slot = a.slots ? a.slots[n] : n;
+    if (t0 < 0 || t1 > a.total || t0 >= t1) return;  // empty, or offsets that are none
     bool run = slot >= 0 && slot < a.n_slots;
     const int row0 = rb * warps * ROWS;
-    const T *qp = static_cast<const T *>(a.q), *kp = static_cast<const T *>(a.k);
     const T *vp = static_cast<const T *>(a.v);
     T *op = static_cast<T *>(a.o);
-
-    // of the sequences with tokens that name one slot the first has it
-    int taken = 0;
-    if (run && a.update && a.slots)
-        for (int i = tid; i < n; i += blockDim.x)
-            if (a.slots[i] == slot) taken |= !a.cu || a.cu[i] < a.cu[i + 1];
 
     const int sub = lane % LW, grp = lane / LW;
     const int wrow = row0 + warp * ROWS;  // the warp's first row
@@ -127,31 +127,33 @@ decode_runs_kernel(RunsArgs a, int row_blocks) {
                           ? load_state<VEC>(state + (long long)row * a.Dk, 4 * (v * LW + sub), a.Dk)
                           : make_float4(0, 0, 0, 0);
         }
-    if (__syncthreads_or(taken)) run = false;
-    if (!run) {  // a row of padding: its outputs are zero, nothing else is touched
-        if (op)
-            for (int t = t0; t < t1; ++t)
-                for (int i = tid; i < warps * ROWS && row0 + i < a.Dv; i += blockDim.x)
-                    op[((long long)t * a.Hv + h) * a.Dv + row0 + i] = from_f32<T>(0.f);
-        return;
-    }
     const int hk = h / (a.Hv / a.Hk);
 
     for (int c0 = t0; c0 < t1; c0 += kTok) {
         const int m = min(kTok, t1 - c0);
-        // k, q (normalised) and the gates of the m tokens
-        for (int j = warp; j < m; j += warps) {
+        // a warp per token: k and q (normalised), v of the block's rows, the gates
+        for (int j = warp; j < m && run; j += warps) {
             const long long t = c0 + j;
-            const T *kr = kp + t * a.k_stride + (long long)hk * a.Dk;
-            const T *qr = qp ? qp + t * a.q_stride + (long long)hk * a.Dk : nullptr;
-            float x[(PD + 31) / 32], y[(PD + 31) / 32], kn = 0.f, qn = 0.f;
+            const T *kr = static_cast<const T *>(a.k) + t * a.k_stride + (long long)hk * a.Dk;
+            const T *qr = a.q ? static_cast<const T *>(a.q) + t * a.q_stride + (long long)hk * a.Dk
+                              : nullptr;
+            const T *vr = vp + t * a.v_stride + (long long)h * a.Dv;
+            float x[E], y[E];
 #pragma unroll
-            for (int i = 0; i < (PD + 31) / 32; ++i) {
+            for (int i = 0; i < E; ++i) {
                 const int c = lane + 32 * i;
                 x[i] = c < a.Dk ? to_f32(kr[c]) : 0.f;
                 y[i] = qr && c < a.Dk ? to_f32(qr[c]) : 0.f;
+            }
+            const float g0 = a.log_alpha[t * a.la_stride + h], g1 = a.beta[t * a.be_stride + h];
+            for (int i = lane; i < warps * ROWS; i += 32)
+                sv[j][i] = row0 + i < a.Dv ? to_f32(vr[row0 + i]) : 0.f;
+            float kn = 0.f, qn = 0.f, kq = 0.f;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
                 kn += x[i] * x[i];
                 qn += y[i] * y[i];
+                kq += x[i] * y[i];
             }
             float rk = 1.f, rq = 1.f;
             if (a.flags & kFlagL2Norm) {
@@ -159,115 +161,193 @@ decode_runs_kernel(RunsArgs a, int row_blocks) {
                 rq = rsqrtf(warp_sum(qn) + kNormEps);
             }
 #pragma unroll
-            for (int i = 0; i < (PD + 31) / 32; ++i) {
+            for (int i = 0; i < E; ++i) {
                 const int c = lane + 32 * i;
                 if (c < PD) {
                     sk[j][c] = rk * x[i];
                     sq[j][c] = rq * y[i];
                 }
             }
+            if (m == 1) kq = warp_sum(kq);
             if (lane == 0) {
-                const float2 gp = gate_pair(a.log_alpha[t * a.la_stride + h],
-                                            a.beta[t * a.be_stride + h], a.flags);
-                al[j] = expf(gp.x);
+                const float2 gp = gate_pair(g0, g1, a.flags);
+                const float alpha = expf(gp.x);
+                al[j] = alpha;
                 be[j] = gp.y;
+                if (m == 1) {
+                    gam[0] = alpha;
+                    tail[0] = 1.f;
+                    tm[0][0][0] = gp.y;
+                    tm[1][0][0] = gp.y * (rk * rq * kq);
+                }
             }
         }
-        __syncthreads();
-        // the tokens' products with one another; thread 0: the decays up to and from each
-        for (int p = warp; p < m * m; p += warps) {
-            const int i = p / m, j = p % m;  // j < i: k_i.k_j, else q_j.k_i (i <= j)
-            const float *x = j < i ? sk[i] : sq[j], *y = j < i ? sk[j] : sk[i];
-            float d = 0.f;
-#pragma unroll
-            for (int c = lane; c < PD; c += 32) d += x[c] * y[c];
-            d = warp_sum(d);
-            if (lane == 0) (j < i ? kk[i][j] : qk[j][i]) = d;
+        if (c0 == t0) {
+            // of the sequences with tokens that name one slot the first has it
+            int taken = 0;
+            if (run && a.update && a.slots)
+                for (int i = tid; i < n; i += blockDim.x)
+                    if (a.slots[i] == slot) taken |= !a.cu || a.cu[i] < a.cu[i + 1];
+            if (__syncthreads_or(taken)) run = false;
+            if (!run) {  // a row of padding: its outputs are zero, nothing else is touched
+                if (op)
+                    for (int t = t0; t < t1; ++t)
+                        for (int i = tid; i < warps * ROWS && row0 + i < a.Dv; i += blockDim.x)
+                            op[((long long)t * a.Hv + h) * a.Dv + row0 + i] = from_f32<T>(0.f);
+                return;
+            }
+        } else {
+            __syncthreads();
         }
-        if (tid == 0) {
-            float g = 1.f;
-            for (int i = 0; i < m; ++i) gam[i] = g *= al[i];
-            g = 1.f;
-            for (int i = m - 1; i >= 0; --i) {
-                tail[i] = g;
-                g *= al[i];
+        if (m > 1) {
+            // a warp per token i: A_ij = beta_i Gamma_ij k_i.k_j (j < i) and
+            // P_ij = Gamma_ij q_i.k_j (j <= i)
+            for (int i = warp; i < m; i += warps) {
+                float x[2 * kTok];
+#pragma unroll
+                for (int j = 0; j < 2 * kTok; ++j) x[j] = 0.f;
+#pragma unroll
+                for (int c = 0; c < E; ++c) {
+                    const int at = lane + 32 * c;
+                    if (at < PD) {
+                        const float ki = sk[i][at], qi = sq[i][at];
+#pragma unroll
+                        for (int j = 0; j < kTok; ++j)
+                            if (j <= i) {
+                                const float kj = sk[j][at];
+                                x[j] += ki * kj;
+                                x[kTok + j] += qi * kj;
+                            }
+                    }
+                }
+                const int w = reduce_scatter<2 * kTok, 32>(x, lane), j = w % kTok;
+                float dec = 1.f;
+                for (int l = j + 1; l <= i; ++l) dec *= al[l];
+                if (lane % 2 == 0 && j <= i) {
+                    if (w < kTok) sA[i][j] = be[i] * dec * x[0];
+                    else sP[i][j] = dec * x[0];
+                }
+                if (lane == 0) {
+                    float g = 1.f;
+                    for (int l = 0; l <= i; ++l) g *= al[l];
+                    gam[i] = g;
+                    g = 1.f;
+                    for (int l = i + 1; l < m; ++l) g *= al[l];
+                    tail[i] = g;
+                }
+            }
+            __syncthreads();
+            if (warp == 0) {  // column j of T = (I + A)^-1 diag(beta), then of M = P T
+                const int j = lane % kTok;
+                float x[kTok];
+#pragma unroll
+                for (int i = 0; i < kTok; ++i) {
+                    x[i] = i == j ? 1.f : 0.f;
+#pragma unroll
+                    for (int l = 0; l < i; ++l)
+                        if (i < m && l >= j) x[i] -= sA[i][l] * x[l];
+                }
+                const float b = j < m ? be[j] : 0.f;
+                for (int i = lane / kTok; i < m; i += 32 / kTok) {
+                    float p = 0.f, xi = 0.f;
+#pragma unroll
+                    for (int l = 0; l < kTok; ++l)
+                        if (l >= j && l <= i) {
+                            p += sP[i][l] * x[l];
+                            if (l == i) xi = x[l];
+                        }
+                    if (j <= i) {
+                        tm[0][i][j] = b * xi;
+                        tm[1][i][j] = b * p;
+                    }
+                }
             }
         }
         // the rows' products with k and q
         for (int j = 0; j < m; ++j) {
-            float x[2 * R];
+            float2 x2[2 * R];
 #pragma unroll
-            for (int i = 0; i < 2 * R; ++i) x[i] = 0.f;
+            for (int i = 0; i < 2 * R; ++i) x2[i] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float4 k4 = *reinterpret_cast<const float4 *>(&sk[j][4 * (v * LW + sub)]);
                 const float4 q4 = *reinterpret_cast<const float4 *>(&sq[j][4 * (v * LW + sub)]);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    x[r] += s[r][v].x * k4.x + s[r][v].y * k4.y + s[r][v].z * k4.z + s[r][v].w * k4.w;
-                    x[R + r] += s[r][v].x * q4.x + s[r][v].y * q4.y + s[r][v].z * q4.z + s[r][v].w * q4.w;
+                    const float2 lo = make_float2(s[r][v].x, s[r][v].y);
+                    const float2 hi = make_float2(s[r][v].z, s[r][v].w);
+                    x2[r] = __ffma2_rn(lo, make_float2(k4.x, k4.y), x2[r]);
+                    x2[r] = __ffma2_rn(hi, make_float2(k4.z, k4.w), x2[r]);
+                    x2[R + r] = __ffma2_rn(lo, make_float2(q4.x, q4.y), x2[R + r]);
+                    x2[R + r] = __ffma2_rn(hi, make_float2(q4.z, q4.w), x2[R + r]);
                 }
             }
+            float x[2 * R];
+#pragma unroll
+            for (int i = 0; i < 2 * R; ++i) x[i] = x2[i].x + x2[i].y;
             const int first = reduce_scatter<2 * R, LW>(x, lane);
             constexpr int NK = 2 * R > LW ? 2 * R / LW : 1;  // sums left in a lane
 #pragma unroll
             for (int i = 0; i < NK; ++i) {
                 const int w = first + i;
-                (w < R ? da[warp][j][grp * R + w] : db[warp][j][grp * R + w - R]) = x[i];
+                (w < R ? ra[warp][grp * R + w][j] : rb_[warp][grp * R + w - R][j]) = x[i];
             }
         }
-        __syncthreads();
-        // each row's corrections u (left in da) and outputs
-        for (int i = lane; i < ROWS; i += 32) {
-            const int row = wrow + i;
-            float u[kTok];
-            if (row < a.Dv) {
+        if (m > 1) __syncthreads();
+        else __syncwarp();
+        // each row's r, then its outputs and corrections
+        for (int i = lane; i < ROWS * kTok; i += 32) {
+            const int row = i / kTok, j = i % kTok;
+            if (j < m) ra[warp][row][j] = sv[j][warp * ROWS + row] - gam[j] * ra[warp][row][j];
+        }
+        __syncwarp();
+        for (int at = lane; at < ROWS * kTok; at += 32) {
+            const int row = at / kTok, i = at % kTok;
+            if (i < m) {
+                float u = 0.f, out = gam[i] * rb_[warp][row][i];
 #pragma unroll
-                for (int t = 0; t < kTok; ++t)
-                    if (t < m) {
-                        const long long tok = c0 + t;
-                        float acc = to_f32(vp[tok * a.v_stride + (long long)h * a.Dv + row]) -
-                                    gam[t] * da[warp][t][i];
-                        float out = gam[t] * db[warp][t][i];
-                        float dec = al[t];
-#pragma unroll
-                        for (int j = kTok - 1; j >= 0; --j)
-                            if (j < t) {
-                                acc -= dec * kk[t][j] * u[j];
-                                out += dec * qk[t][j] * u[j];
-                                dec *= al[j];
-                            }
-                        u[t] = be[t] * acc;
-                        if (op)
-                            op[(tok * a.Hv + h) * a.Dv + row] = from_f32<T>(out + qk[t][t] * u[t]);
-                        da[warp][t][i] = tail[t] * u[t];
+                for (int j = 0; j < kTok; ++j)
+                    if (j <= i) {
+                        const float r = ra[warp][row][j];
+                        u += tm[0][i][j] * r;
+                        out += tm[1][i][j] * r;
                     }
-            } else {
-                for (int t = 0; t < m; ++t) da[warp][t][i] = 0.f;
+                su[warp][i][row] = tail[i] * u;
+                if (op && wrow + row < a.Dv)
+                    op[((long long)(c0 + i) * a.Hv + h) * a.Dv + wrow + row] = from_f32<T>(out);
             }
         }
         __syncwarp();
         if (a.update || c0 + kTok < t1) {
-            const float g = gam[m - 1];
+            const float g1 = gam[m - 1];
+            const float2 g = make_float2(g1, g1);
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    s[r][v].x *= g; s[r][v].y *= g; s[r][v].z *= g; s[r][v].w *= g;
+                    const float2 lo = __fmul2_rn(make_float2(s[r][v].x, s[r][v].y), g);
+                    const float2 hi = __fmul2_rn(make_float2(s[r][v].z, s[r][v].w), g);
+                    s[r][v] = make_float4(lo.x, lo.y, hi.x, hi.y);
                 }
-            for (int j = 0; j < m; ++j)
+            for (int j = 0; j < m; ++j) {
+                const float4 u4 = *reinterpret_cast<const float4 *>(&su[warp][j][grp * R]);
+                const float u[R] = {u4.x, u4.y, u4.z, u4.w};
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     const float4 k4 = *reinterpret_cast<const float4 *>(&sk[j][4 * (v * LW + sub)]);
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
-                        const float u = da[warp][j][grp * R + r];
-                        s[r][v].x += u * k4.x; s[r][v].y += u * k4.y;
-                        s[r][v].z += u * k4.z; s[r][v].w += u * k4.w;
+                        const float2 uu = make_float2(u[r], u[r]);
+                        const float2 lo = __ffma2_rn(uu, make_float2(k4.x, k4.y),
+                                                     make_float2(s[r][v].x, s[r][v].y));
+                        const float2 hi = __ffma2_rn(uu, make_float2(k4.z, k4.w),
+                                                     make_float2(s[r][v].z, s[r][v].w));
+                        s[r][v] = make_float4(lo.x, lo.y, hi.x, hi.y);
                     }
                 }
+            }
         }
-        __syncthreads();  // the tokens' shared arrays are written again
+        if (c0 + kTok < t1) __syncthreads();  // the tokens' shared arrays are written again
     }
     if (!a.update) return;
 #pragma unroll
@@ -282,7 +362,7 @@ decode_runs_kernel(RunsArgs a, int row_blocks) {
 
 template <typename T, int LW, int V>
 cudaError_t launch(const RunsArgs &a, cudaStream_t st) {
-    constexpr int ROWS = (V == 1 ? 8 : 4) * (32 / LW);
+    constexpr int ROWS = kRows<LW>;
     const int warps = min(kMaxWarps, (a.Dv + ROWS - 1) / ROWS);
     const int row_blocks = (a.Dv + warps * ROWS - 1) / (warps * ROWS);
     const unsigned blocks = (unsigned)((long long)a.N * a.Hv * row_blocks);
@@ -296,9 +376,9 @@ cudaError_t launch(const RunsArgs &a, cudaStream_t st) {
 template <typename T>
 cudaError_t launch_t(const RunsArgs &a, cudaStream_t st) {
     if (a.Dk <= 16) return launch<T, 4, 1>(a, st);
-    if (a.Dk <= 32) return launch<T, 8, 1>(a, st);
-    if (a.Dk <= 64) return launch<T, 16, 1>(a, st);
-    if (a.Dk <= 128) return launch<T, 32, 1>(a, st);
+    if (a.Dk <= 32) return launch<T, 4, 2>(a, st);
+    if (a.Dk <= 64) return launch<T, 8, 2>(a, st);
+    if (a.Dk <= 128) return launch<T, 16, 2>(a, st);
     return launch<T, 32, 2>(a, st);
 }
 
