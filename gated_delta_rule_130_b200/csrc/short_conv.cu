@@ -7,10 +7,10 @@
 //     dw[c, j] = sum_t dz[t] x[t - (W - 1) + j],   dbias = sum_t dz[t].
 //
 // Both directions are bound by HBM: x is read and y written once (backward: dy, x and
-// dx).  A thread owns 16 bytes' worth of channels (forward) and walks a tile of
-// tokens with the last W inputs in registers; the W - 1 inputs before a tile are read
-// again.  Sums are float32; dw is summed per tile and then over the tiles, in one
-// order.
+// dx).  A thread owns four neighbouring channels and walks a tile of tokens with the
+// last W inputs in registers, the rows of the next tokens on their way; the W - 1 rows
+// before a tile are read again.  Sums are float32; dw is summed per tile and then over
+// the tiles, in one order.
 #include "kernels.h"
 #include "vec.cuh"
 
@@ -35,7 +35,7 @@ __device__ __forceinline__ int seq_of(const int *cu, int N, int t, int lane) {
     return lo;
 }
 
-// What a lane knows of token t0 + lane (or t0 - (W - 1) + lane): its sequence's span.
+// The sequence of token t, known to lie in [lo, hi].
 struct Span {
     int n, start, end;  // start >= end: not in a sequence
 };
@@ -61,237 +61,336 @@ __device__ __forceinline__ int part_of(const ConvArgs &a, int c) {
     return p;
 }
 
+// w[j][e] = weight[c + e, j]: VEC * W consecutive parameters, in vectors where VEC > 1.
+template <typename P, int VEC, int W>
+__device__ __forceinline__ void load_taps(const P *p, float (&w)[W][VEC]) {
+    constexpr int V = VEC > 1 ? 4 : 1;
+#pragma unroll
+    for (int i = 0; i < VEC * W / V; ++i) {
+        float x[V];
+        load_vec<P, V>(p + i * V, x);
+#pragma unroll
+        for (int e = 0; e < V; ++e) w[(i * V + e) % W][(i * V + e) / W] = x[e];
+    }
+}
 template <typename T, int VEC, int W>
 __device__ __forceinline__ void load_weights(const ConvArgs &a, int c, float (&w)[W][VEC],
                                              float (&b)[VEC]) {
+    if (a.weight_f32) load_taps<float, VEC, W>(static_cast<const float *>(a.weight) + (long long)c * W, w);
+    else load_taps<T, VEC, W>(static_cast<const T *>(a.weight) + (long long)c * W, w);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-            float x[1];
-            load_param<T, 1>(a.weight, (long long)(c + e) * W + j, a.weight_f32, x);
-            w[j][e] = x[0];
-        }
-        b[e] = 0.f;
-        if (a.bias) {
-            float x[1];
-            load_param<T, 1>(a.bias, c + e, a.weight_f32, x);
-            b[e] = x[0];
-        }
+    for (int e = 0; e < VEC; ++e) b[e] = 0.f;
+    if (a.bias) {
+        if (a.weight_f32) load_vec<float, VEC>(static_cast<const float *>(a.bias) + c, b);
+        else load_vec<T, VEC>(static_cast<const T *>(a.bias) + c, b);
     }
 }
 
-// Forward.  A block: kThreads * VEC channels and the tokens [t0, t0 + TT).  The
-// block that holds a sequence's first token also takes the sequence's next W - 2
-// tokens, where they lie behind its tile, and no other block does: so the held inputs
-// of a slot are read and written by one thread only.
+// Forward.  A block: kThreads * VEC channels and the tokens [t0, t0 + TT).  The block that
+// holds a sequence's first token also takes the sequence's next W - 2 tokens, where
+// they lie behind its tile, and no other block does: so the held inputs of a slot are
+// read and written by one thread only.
+constexpr int kMine = 1, kPadding = 2, kFirst = 4, kHold = 8;
+struct __align__(16) Token {  // what a block knows of one of its tokens
+    int flags, start, end, slot;
+};
+
 template <typename T, int VEC, int W, int TT>
 __global__ void __launch_bounds__(kThreads)
 conv_fwd(ConvArgs a, unsigned ctiles) {
-    static_assert(TT + W - 2 <= 32, "a lane per token");
-    const int lane = threadIdx.x % 32;
-    const int c = (int)((blockIdx.x % ctiles * kThreads + threadIdx.x) * VEC);
+    constexpr int NT = TT + W - 2;          // the tile and the tokens behind it
+    constexpr int B = NT < 8 ? NT : 8;      // rows loaded at once
+    static_assert(NT <= kThreads, "a thread per token");
+    __shared__ Token tok[NT];
+    __shared__ int seq[NT];
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int c = (int)((blockIdx.x % ctiles * kThreads + tid) * VEC);
     const int t0 = (int)(blockIdx.x / ctiles * TT), t1 = min(t0 + TT, a.total);
-    // lane i: token t0 + i, its sequence and whether this block takes it
     const int far = min(t1 + W - 2, a.total) - 1;
-    int lo = 0, hi = 0;
-    if (a.cu) {
-        lo = seq_of(a.cu, a.N, t0, lane);
-        hi = seq_of(a.cu, a.N, far, lane);
-    }
-    const int t_mine = t0 + lane;
-    Span sp = span_of(a, t_mine <= far ? t_mine : -1, lo, hi);
-    int slot = -1;
-    bool mine = sp.start < sp.end;
-    if (mine) {
-        const bool heads_here = sp.start >= t0 && sp.start < t1;
-        mine = t_mine - sp.start < W - 1 ? heads_here : t_mine < t1;
-        if (a.states) {
-            slot = a.slots ? a.slots[sp.n] : sp.n;
-            if (slot >= a.n_slots) slot = -1;
-        }
-    }
-    // of the sequences with tokens that name one slot the first has it
-    bool padding = a.states && slot < 0;
-    if (a.states && a.slots) {
-        unsigned todo = __ballot_sync(0xffffffffu, mine && !padding);
-        while (todo) {
-            const int i = __ffs(todo) - 1;
-            const int n = __shfl_sync(0xffffffffu, sp.n, i);
-            const int want = __shfl_sync(0xffffffffu, slot, i);
-            int taken = 0;
-            for (int k = lane; k < n; k += 32)
-                if (a.slots[k] == want) taken |= !a.cu || a.cu[k] < a.cu[k + 1];
-            taken = __any_sync(0xffffffffu, taken);
-            if (sp.n == n) padding |= taken;
-            todo &= ~__ballot_sync(0xffffffffu, sp.n == n);
-        }
-    }
-    const int flags = (mine ? 1 : 0) | (padding ? 2 : 0);
-
     const bool live = c < a.C;
     const int cc = live ? c : 0;
     const T *x = static_cast<const T *>(a.x) + cc;
+
+    // the inputs before the tile and its first rows are on their way while the
+    // sequences are found
+    Raw<T, VEC> cur[B];
+    float win[W - 1][VEC];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+        const int s = t0 - (W - 1) + j;
+        if (s >= 0) load_vec<T, VEC>(x + s * a.x_stride, win[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+        if (t0 + i <= far) cur[i] = load_raw<T, VEC>(x + (t0 + i) * a.x_stride);
+
+    if (warp * 32 < NT) {
+        int lo = 0, hi = 0;
+        if (a.cu) {
+            lo = seq_of(a.cu, a.N, t0, lane);
+            hi = seq_of(a.cu, a.N, far, lane);
+        }
+        if (tid < NT) {
+            const int t = t0 + tid;
+            const Span sp = span_of(a, t <= far ? t : -1, lo, hi);
+            Token k{0, sp.start, sp.end, -1};
+            if (sp.start < sp.end) {
+                const int pos = t - sp.start;
+                const bool head = sp.start >= t0 && sp.start < t1;
+                if (pos < W - 1 ? head : t < t1) k.flags |= kMine;
+                if (pos == 0) k.flags |= kFirst;
+                if (a.states) {
+                    k.slot = a.slots ? a.slots[sp.n] : sp.n;
+                    if (k.slot < 0 || k.slot >= a.n_slots) k.flags |= kPadding;
+                    // with the last token that needs them the held inputs give way
+                    else if (t == min(sp.start + W - 2, sp.end - 1)) k.flags |= kHold;
+                }
+            }
+            tok[tid] = k;
+            seq[tid] = sp.start < sp.end ? sp.n : -1;
+        }
+    }
+    __syncthreads();
+    if (a.states && a.slots) {
+        // of the sequences with tokens that name one slot the first has it
+        for (int i = warp; i < NT; i += kThreads / 32) {
+            const int n = seq[i];
+            if (n < 0 || (i > 0 && seq[i - 1] == n) || (tok[i].flags & kPadding)) continue;
+            const int want = tok[i].slot;
+            int taken = 0;
+            for (int k = lane; k < n; k += 32)
+                if (a.slots[k] == want) taken |= !a.cu || a.cu[k] < a.cu[k + 1];
+            if (__any_sync(0xffffffffu, taken))
+                for (int k = i + lane; k < NT; k += 32)
+                    if (seq[k] == n) tok[k].flags |= kPadding;
+        }
+        __syncthreads();
+    }
+    if (!live) return;
+    int count = t1 - t0;
+#pragma unroll
+    for (int i = TT; i < NT; ++i)
+        if (t1 - t0 == TT && (tok[i].flags & kMine)) count = i + 1;
+
     const int p = part_of(a, cc);
-    T *y = static_cast<T *>(a.part[p]) + (cc - a.begin[p]);
+    T *y = static_cast<T *>(a.part[p]) + (cc - a.begin[p]) + t0 * a.part_stride[p];
     float w[W][VEC], b[VEC];
     load_weights<T, VEC, W>(a, cc, w, b);
-    float win[W][VEC];  // the inputs t - (W - 1) .. t
-    int at = -1;        // the token that win ends with
-    for (int i = 0; i < TT + W - 2; ++i) {
-        const int t = t0 + i;
-        const int f = __shfl_sync(0xffffffffu, flags, i);
-        const int start = __shfl_sync(0xffffffffu, sp.start, i);
-        const int end = __shfl_sync(0xffffffffu, sp.end, i);
-        const int sl = __shfl_sync(0xffffffffu, slot, i);
-        if (!(f & 1) || !live) continue;
-        if (f & 2) {
+    for (int i0 = 0; i0 < count; i0 += B) {
+        Raw<T, VEC> next[B];
+        if (i0 + B < count) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) win[W - 1][e] = 0.f;
-            store_vec(y + t * a.part_stride[p], win[W - 1]);
-            continue;
+            for (int i = 0; i < B; ++i)
+                if (t0 + i0 + B + i <= far)
+                    next[i] = load_raw<T, VEC>(x + (t0 + i0 + B + i) * a.x_stride);
         }
-        T *held = a.states ? static_cast<T *>(a.states) + (long long)sl * (W - 1) * a.C + cc : nullptr;
-        if (at == t - 1 && t > start) {
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j)
+        for (int i = 0; i < B; ++i) {
+            if (i0 + i < count) {
+                const int f = tok[i0 + i].flags;
+                T *held = nullptr;
+                if (f & (kFirst | kHold)) {
+                    if (a.states && !(f & kPadding))
+                        held = static_cast<T *>(a.states) +
+                               (long long)tok[i0 + i].slot * (W - 1) * a.C + cc;
+                    if (f & kFirst) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
-        } else {  // a new sequence, or the tile begins inside one
+                        for (int j = 0; j < W - 1; ++j) {
+                            if (held) {
+                                load_vec<T, VEC>(held + (long long)j * a.C, win[j]);
+                            } else {
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) {
-                const int s = t - (W - 1) + j;
-                if (s >= start) {
-                    load_vec<T, VEC>(x + s * a.x_stride, win[j]);
-                } else if (held) {
-                    load_vec<T, VEC>(held + (long long)(W - 1 + s - start) * a.C, win[j]);
-                } else {
+                                for (int e = 0; e < VEC; ++e) win[j][e] = 0.f;
+                            }
+                        }
+                    }
+                }
+                float now[VEC], z[VEC];
+                widen(cur[i], now);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) win[j][e] = 0.f;
+                for (int e = 0; e < VEC; ++e) z[e] = b[e];
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) fma_vec<VEC>(w[j], win[j], z);
+                fma_vec<VEC>(w[W - 1], now, z);
+                if (f & kMine) {
+                    if (a.silu) {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) z[e] *= fast_sigmoid(z[e]);
+                    }
+                    if (f & kPadding) {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) z[e] = 0.f;
+                    }
+                    store_vec(y, z);
+                }
+                y += a.part_stride[p];
+#pragma unroll
+                for (int j = 0; j + 1 < W - 1; ++j)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) win[W - 2][e] = now[e];
+                if (held && (f & kMine) && (f & kHold)) {
+                    // the sequence's last inputs; win has them where it is that short
+                    const int end = tok[i0 + i].end;
+                    const bool is_short = end - tok[i0 + i].start < W - 1;
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) {
+                        float v[VEC];
+                        if (is_short) {
+#pragma unroll
+                            for (int e = 0; e < VEC; ++e) v[e] = win[j][e];
+                        } else {
+                            load_vec<T, VEC>(x + (end - (W - 1) + j) * a.x_stride, v);
+                        }
+                        store_vec(held + (long long)j * a.C, v);
+                    }
                 }
             }
         }
-        load_vec<T, VEC>(x + t * a.x_stride, win[W - 1]);
-        at = t;
-        float out[VEC];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            float z = b[e];
-#pragma unroll
-            for (int j = 0; j < W; ++j) z += w[j][e] * win[j][e];
-            out[e] = a.silu ? z * fast_sigmoid(z) : z;
-        }
-        store_vec(y + t * a.part_stride[p], out);
-        // with the last token that needs them the held inputs give way to the
-        // sequence's last ones (win still holds the older ones of a short sequence)
-        if (held && t == min(start + W - 2, end - 1)) {
-            const int len = end - start;
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) {
-                float v[VEC];
-                if (len >= W - 1) {
-                    load_vec<T, VEC>(x + (end - (W - 1) + j) * a.x_stride, v);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) v[e] = win[j + 1][e];
-                }
-                store_vec(held + (long long)j * a.C, v);
-            }
-        }
+        for (int i = 0; i < B; ++i) cur[i] = next[i];
     }
 }
 
-constexpr int kBwdTokens = 128;  // tokens per block
+constexpr int kMaxTile = 1024;  // tokens per block of the backward
 
-// Backward.  A block: kThreads * VEC channels and the tokens [t0, t0 + kBwdTokens): their
-// dx (dz of the W - 1 tokens behind the tile is formed again) and their share of dw.
+// Backward.  A block: kThreads * VEC channels and the tokens [t0, t0 + tile): their dx
+// (dz of the W - 1 tokens behind the tile is formed again) and their share of dw.
 template <typename T, int VEC, int W>
 __global__ void __launch_bounds__(kThreads)
-conv_bwd(ConvArgs a, unsigned ctiles) {
+conv_bwd(ConvArgs a, unsigned ctiles, int tile) {
+    constexpr int B = 4;  // rows loaded at once
+    // of each token of the tile and behind it: how many inputs of its sequence lie
+    // before it (W - 1 at most), -1 where it is in none
+    __shared__ signed char before[kMaxTile + W - 1];
     const int lane = threadIdx.x % 32;
     const int c = (int)((blockIdx.x % ctiles * kThreads + threadIdx.x) * VEC);
-    const int tile = (int)(blockIdx.x / ctiles);
-    const int t0 = tile * kBwdTokens, t1 = min(t0 + kBwdTokens, a.total);
+    const int t0 = (int)(blockIdx.x / ctiles) * tile, t1 = min(t0 + tile, a.total);
+    const int stop = min(t1 + W - 1, a.total);  // tokens whose dz is formed
     const bool live = c < a.C;
     const int cc = live ? c : 0;
     const T *x = static_cast<const T *>(a.x) + cc;
     const int p = part_of(a, cc);
     const T *dy = static_cast<const T *>(a.part[p]) + (cc - a.begin[p]);
-    T *dx = static_cast<T *>(a.dx) + cc;
-    float w[W][VEC], b[VEC], dw[W][VEC], db[VEC];
+    const long long dy_stride = a.part_stride[p];
+
+    float win[W - 1][VEC];  // the inputs before the token
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+        const int s = t0 - (W - 1) + j;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) win[j][e] = 0.f;
+        if (s >= 0) load_vec<T, VEC>(x + s * a.x_stride, win[j]);
+    }
+    Raw<T, VEC> cx[B], cd[B];
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+        if (t0 + i < stop) {
+            cx[i] = load_raw<T, VEC>(x + (t0 + i) * a.x_stride);
+            cd[i] = load_raw<T, VEC>(dy + (t0 + i) * dy_stride);
+        }
+    {
+        int lo = 0, hi = 0;
+        if (a.cu) {
+            lo = seq_of(a.cu, a.N, t0, lane);
+            hi = seq_of(a.cu, a.N, stop - 1, lane);
+        }
+        for (int t = t0 + threadIdx.x; t < stop; t += kThreads) {
+            const Span sp = span_of(a, t, lo, hi);
+            before[t - t0] = sp.start < sp.end ? min(t - sp.start, W - 1) : -1;
+        }
+    }
+    float w[W][VEC], b[VEC], dw[W][VEC], db[VEC], acc[W][VEC];
     load_weights<T, VEC, W>(a, cc, w, b);
-    float win[W][VEC], acc[W][VEC];  // acc[j]: dx of token t - (W - 1) + j so far
 #pragma unroll
     for (int j = 0; j < W; ++j)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) win[j][e] = acc[j][e] = dw[j][e] = 0.f;
+        for (int e = 0; e < VEC; ++e) acc[j][e] = dw[j][e] = 0.f;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) db[e] = 0.f;
-    int n = a.cu ? seq_of(a.cu, a.N, t0, lane) : t0;
-    Span sp = span_of(a, t0, n, n);
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) {  // the inputs before the tile
-        const int s = t0 - (W - 1) + j;
-        if (live && s >= 0) load_vec<T, VEC>(x + s * a.x_stride, win[j + 1]);
-    }
-    for (int t = t0; t < t1 + W - 1; ++t) {
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                win[j][e] = win[j + 1][e];
-                acc[j][e] = acc[j + 1][e];
-            }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[W - 1][e] = 0.f;
-        if (t < a.total && t >= sp.end) {  // the next sequence
-            if (a.cu) {
-                if (n + 1 < a.N && a.cu[n + 1] <= t && a.cu[n + 2] > t) ++n;
-                else n = seq_of(a.cu, a.N, t, lane);
-                sp = span_of(a, t, n, n);
-            } else {
-                sp = Span{t, t, t + 1};
-            }
-        }
-        if (t < a.total && sp.start < sp.end && live) {
-            float d[VEC];
-            load_vec<T, VEC>(x + t * a.x_stride, win[W - 1]);
-            load_vec<T, VEC>(dy + t * a.part_stride[p], d);
-            float in[W][VEC];  // the inputs of t's sequence only
-#pragma unroll
-            for (int j = 0; j < W; ++j)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    in[j][e] = t - (W - 1) + j >= sp.start ? win[j][e] : 0.f;
-            if (a.silu) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    float z = b[e];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) z += w[j][e] * in[j][e];
-                    const float sig = fast_sigmoid(z);
-                    d[e] *= sig * (1.f + z * (1.f - sig));
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < W; ++j)
-                if (t - (W - 1) + j >= sp.start)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) acc[j][e] += w[j][e] * d[e];
-            if (t < t1) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    db[e] += d[e];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) dw[j][e] += d[e] * in[j][e];
-                }
-            }
-        }
-        const int done = t - (W - 1);
-        if (live && done >= t0 && done < t1) store_vec(dx + (long long)done * a.C, acc[0]);
-    }
+    __syncthreads();
     if (!live) return;
-    float *mine = a.partial + (long long)tile * a.C * (W + 1);
+    // acc[j]: dx of token t - (W - 1) + j so far; it leaves with the last token that
+    // reads the input
+    T *dx = static_cast<T *>(a.dx) + cc + (t0 - (W - 1)) * (long long)a.C;
+    for (int i0 = t0; i0 < t1 + W - 1; i0 += B) {
+        Raw<T, VEC> nx[B], nd[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+            if (i0 + B + i < stop) {
+                nx[i] = load_raw<T, VEC>(x + (i0 + B + i) * a.x_stride);
+                nd[i] = load_raw<T, VEC>(dy + (i0 + B + i) * dy_stride);
+            }
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int t = i0 + i;
+            const int have = t < stop ? before[t - t0] : -1;
+            if (have >= 0) {
+                float in[W][VEC], d[VEC];
+                widen(cx[i], in[W - 1]);
+                widen(cd[i], d);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) in[j][e] = win[j][e];
+                if (have < W - 1) {  // near the sequence's first token
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e)
+                            if (W - 1 - j > have) in[j][e] = 0.f;
+                }
+                if (a.silu) {
+                    float z[VEC];
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) z[e] = b[e];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) fma_vec<VEC>(w[j], in[j], z);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float sig = fast_sigmoid(z[e]);
+                        d[e] *= fmaf(sig, fmaf(-z[e], sig, z[e]), sig);
+                    }
+                }
+                if (have < W - 1) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        if (W - 1 - j <= have) fma_vec<VEC>(w[j], d, acc[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) fma_vec<VEC>(w[j], d, acc[j]);
+                }
+                if (t < t1) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) db[e] += d[e];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) fma_vec<VEC>(d, in[j], dw[j]);
+                }
+#pragma unroll
+                for (int j = 0; j + 1 < W - 1; ++j)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) win[W - 2][e] = in[W - 1][e];
+            }
+            const int done = t - (W - 1);
+            if (done >= t0 && done < t1) store_vec(dx, acc[0]);
+            dx += a.C;
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) acc[j][e] = acc[j + 1][e];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) acc[W - 1][e] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            cx[i] = nx[i];
+            cd[i] = nd[i];
+        }
+    }
+    float *mine = a.partial + (long long)(blockIdx.x / ctiles) * a.C * (W + 1);
 #pragma unroll
     for (int j = 0; j < W; ++j)
 #pragma unroll
@@ -300,86 +399,104 @@ conv_bwd(ConvArgs a, unsigned ctiles) {
     for (int e = 0; e < VEC; ++e) mine[(long long)W * a.C + c + e] = db[e];
 }
 
-// dw[c, j] and db[c] = sums over the tiles' partial sums, always in the same order.
+// dw[c, j] and db[c] = sums over the tiles' partial sums, always in the same order:
+// eight threads take every eighth tile each.
 __global__ void __launch_bounds__(256)
 conv_bwd_sum(const float *partial, float *dw, float *db, int tiles, int C, int W) {
-    const int i = blockIdx.x * 256 + threadIdx.x;  // j * C + c
-    if (i >= (W + (db ? 1 : 0)) * C) return;
+    __shared__ float part[8][33];
+    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
+    const long long i = (long long)blockIdx.x * 32 + tx;  // j * C + c
+    const bool in = i < (long long)(W + (db ? 1 : 0)) * C;
     float s = 0.f;
-    for (int k = 0; k < tiles; ++k) s += partial[(long long)k * C * (W + 1) + i];
-    const int j = i / C, c = i % C;
+    if (in)
+#pragma unroll 4
+        for (int k = ty; k < tiles; k += 8) s += partial[(long long)k * C * (W + 1) + i];
+    part[ty][tx] = s;
+    __syncthreads();
+    if (ty || !in) return;
+#pragma unroll
+    for (int k = 1; k < 8; ++k) s += part[k][tx];
+    const int j = (int)(i / C), c = (int)(i % C);
     if (j < W) dw[(long long)c * W + j] = s;
     else db[c] = s;
 }
 
-template <typename T>
+template <typename T, int VEC>
 bool vectors_fit(const ConvArgs &a) {
+    constexpr size_t bytes = VEC * sizeof(T);
     const auto fits = [](const void *p, long long stride) {
-        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * (int)sizeof(T) % 16 == 0;
+        return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * sizeof(T) % bytes == 0;
     };
-    bool ok = fits(a.x, a.x_stride) && fits(a.states, a.C) && fits(a.dx, a.C);
+    bool ok = a.C % VEC == 0 && fits(a.x, a.x_stride) && fits(a.states, a.C) && fits(a.dx, a.C);
     for (int p = 0; p < a.parts; ++p)
-        ok = ok && fits(a.part[p], a.part_stride[p]) && a.begin[p] * sizeof(T) % 16 == 0;
-    return ok && a.C * sizeof(T) % 16 == 0;
+        ok = ok && fits(a.part[p], a.part_stride[p]) && a.begin[p] % VEC == 0;
+    return ok;
 }
+
+unsigned channel_tiles(int C, int vec) { return (C + kThreads * vec - 1) / (kThreads * vec); }
 
 template <typename T, int VEC, int W>
 cudaError_t fwd_w(const ConvArgs &a, cudaStream_t st) {
-    const unsigned bx = (a.C + kThreads * VEC - 1) / (kThreads * VEC);
-    if ((long long)bx * a.total <= 148 * 16) {
-        conv_fwd<T, VEC, W, 1><<<bx * a.total, kThreads, 0, st>>>(a, bx);
+    const unsigned ct = channel_tiles(a.C, VEC);
+    if ((long long)ct * a.total <= 148 * 32) {
+        conv_fwd<T, VEC, W, 1><<<ct * a.total, kThreads, 0, st>>>(a, ct);
     } else {
-        conv_fwd<T, VEC, W, 16><<<bx * ((a.total + 15) / 16), kThreads, 0, st>>>(a, bx);
+        conv_fwd<T, VEC, W, 32><<<ct * ((a.total + 31) / 32), kThreads, 0, st>>>(a, ct);
     }
     return cudaPeekAtLastError();
+}
+
+// Tokens per block of the backward: blocks of 5 channels-of-128-threads per SM fill the
+// GPU once.  Sized for vectors of 4 channels whatever the call's alignment is, so that
+// the workspace depends on the sizes alone.
+int bwd_tile(int total, int C) {
+    const int ct = (int)channel_tiles(C, 4), rows = 148 * 5 / ct > 1 ? 148 * 5 / ct : 1;
+    const int tile = (total + rows - 1) / rows;
+    return tile < 16 ? 16 : tile > kMaxTile ? kMaxTile : tile;
 }
 
 template <typename T, int VEC, int W>
 cudaError_t bwd_w(const ConvArgs &a, cudaStream_t st) {
-    const int tiles = (a.total + kBwdTokens - 1) / kBwdTokens;
-    const unsigned bx = (a.C + kThreads * VEC - 1) / (kThreads * VEC);
-    conv_bwd<T, VEC, W><<<bx * tiles, kThreads, 0, st>>>(a, bx);
-    const int sums = (W + (a.db ? 1 : 0)) * a.C;
-    conv_bwd_sum<<<(sums + 255) / 256, 256, 0, st>>>(a.partial, a.dw, a.db, tiles, a.C, W);
+    const int tile = bwd_tile(a.total, a.C), tiles = (a.total + tile - 1) / tile;
+    const unsigned ct = channel_tiles(a.C, VEC);
+    conv_bwd<T, VEC, W><<<ct * tiles, kThreads, 0, st>>>(a, ct, tile);
+    const long long sums = (long long)(W + (a.db ? 1 : 0)) * a.C;
+    conv_bwd_sum<<<(unsigned)((sums + 31) / 32), 256, 0, st>>>(a.partial, a.dw, a.db, tiles, a.C, W);
     return cudaPeekAtLastError();
 }
+
+#define GDN_CONV(F, T, VEC)                   \
+    switch (a.W) {                            \
+        case 2: return F<T, VEC, 2>(a, st);   \
+        case 3: return F<T, VEC, 3>(a, st);   \
+        default: return F<T, VEC, 4>(a, st);  \
+    }
 
 }  // namespace
 
 cudaError_t launch_short_conv_fwd(const ConvArgs &a, bool bf16, cudaStream_t st) {
-#define GDN_CONV(T, VEC)                                 \
-    switch (a.W) {                                       \
-        case 2: return fwd_w<T, VEC, 2>(a, st);          \
-        case 3: return fwd_w<T, VEC, 3>(a, st);          \
-        default: return fwd_w<T, VEC, 4>(a, st);         \
-    }
     if (bf16) {
-        if (vectors_fit<__nv_bfloat16>(a)) GDN_CONV(__nv_bfloat16, 8)
-        GDN_CONV(__nv_bfloat16, 1)
+        if (vectors_fit<__nv_bfloat16, 4>(a)) GDN_CONV(fwd_w, __nv_bfloat16, 4)
+        GDN_CONV(fwd_w, __nv_bfloat16, 1)
     }
-    if (vectors_fit<float>(a)) GDN_CONV(float, 4)
-    GDN_CONV(float, 1)
-#undef GDN_CONV
+    if (vectors_fit<float, 4>(a)) GDN_CONV(fwd_w, float, 4)
+    GDN_CONV(fwd_w, float, 1)
 }
 
 size_t short_conv_bwd_bytes(int total, int C, int W) {
-    return (size_t)((total + kBwdTokens - 1) / kBwdTokens) * C * (W + 1) * sizeof(float);
+    const int tile = bwd_tile(total, C);
+    return (size_t)((total + tile - 1) / tile) * C * (W + 1) * sizeof(float);
 }
 
 cudaError_t launch_short_conv_bwd(const ConvArgs &a, bool bf16, cudaStream_t st) {
-#define GDN_CONV(T, VEC)                                 \
-    switch (a.W) {                                       \
-        case 2: return bwd_w<T, VEC, 2>(a, st);          \
-        case 3: return bwd_w<T, VEC, 3>(a, st);          \
-        default: return bwd_w<T, VEC, 4>(a, st);         \
-    }
     if (bf16) {
-        if (vectors_fit<__nv_bfloat16>(a)) GDN_CONV(__nv_bfloat16, 8)
-        GDN_CONV(__nv_bfloat16, 1)
+        if (vectors_fit<__nv_bfloat16, 4>(a)) GDN_CONV(bwd_w, __nv_bfloat16, 4)
+        GDN_CONV(bwd_w, __nv_bfloat16, 1)
     }
-    if (vectors_fit<float>(a)) GDN_CONV(float, 4)
-    GDN_CONV(float, 1)
-#undef GDN_CONV
+    if (vectors_fit<float, 4>(a)) GDN_CONV(bwd_w, float, 4)
+    GDN_CONV(bwd_w, float, 1)
 }
+
+#undef GDN_CONV
 
 }  // namespace gdn

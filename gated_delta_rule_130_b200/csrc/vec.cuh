@@ -1,5 +1,5 @@
-// Vectors of consecutive elements widened to float32: VEC = 16 bytes' worth (8
-// bf16, 4 float32), or 1 where an address is not a multiple of 16 bytes.
+// Vectors of consecutive elements widened to float32: VEC = 4 or 8 bf16 or 4 float32
+// at addresses that are multiples of the vector, or 1 element.
 #pragma once
 
 #include "common.cuh"
@@ -9,6 +9,7 @@ namespace gdn {
 template <typename T, int VEC> struct Raw;  // what one load brings
 template <> struct Raw<float, 4> { float4 r; };
 template <> struct Raw<__nv_bfloat16, 8> { uint4 r; };
+template <> struct Raw<__nv_bfloat16, 4> { uint2 r; };
 template <> struct Raw<float, 1> { float r; };
 template <> struct Raw<__nv_bfloat16, 1> { __nv_bfloat16 r; };
 
@@ -27,6 +28,12 @@ __device__ __forceinline__ void widen(const Raw<__nv_bfloat16, 8> &v, float (&x)
         x[2 * i] = __uint_as_float(w[i] << 16);
         x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
+}
+__device__ __forceinline__ void widen(const Raw<__nv_bfloat16, 4> &v, float (&x)[4]) {
+    x[0] = __uint_as_float(v.r.x << 16);
+    x[1] = __uint_as_float(v.r.x & 0xffff0000u);
+    x[2] = __uint_as_float(v.r.y << 16);
+    x[3] = __uint_as_float(v.r.y & 0xffff0000u);
 }
 __device__ __forceinline__ void widen(const Raw<float, 1> &v, float (&x)[1]) { x[0] = v.r; }
 __device__ __forceinline__ void widen(const Raw<__nv_bfloat16, 1> &v, float (&x)[1]) {
@@ -50,6 +57,12 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const float (&x)[8])
     }
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
+__device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const float (&x)[4]) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(x[2], x[3]);
+    *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                                               *reinterpret_cast<const uint32_t *>(&hi));
+}
 template <typename T>
 __device__ __forceinline__ void store_vec(T *p, const float (&x)[1]) { *p = from_f32<T>(x[0]); }
 
@@ -64,10 +77,30 @@ __device__ __forceinline__ void load_param(const void *p, long long at, bool f32
     }
 }
 
-// 1 / (1 + e^-x) by the fast exponential and reciprocal: off by at most a few
+// acc += x y, two elements per instruction.
+template <int VEC>
+__device__ __forceinline__ void fma_vec(const float (&x)[VEC], const float (&y)[VEC],
+                                        float (&acc)[VEC]) {
+    if constexpr (VEC % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+            const float2 z = __ffma2_rn(make_float2(x[e], x[e + 1]), make_float2(y[e], y[e + 1]),
+                                        make_float2(acc[e], acc[e + 1]));
+            acc[e] = z.x;
+            acc[e + 1] = z.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] = fmaf(x[e], y[e], acc[e]);
+    }
+}
+
+// 1 / (1 + e^-x) by the approximate power of two and reciprocal: off by at most a few
 // float32 roundings (1e-6 relative for |x| up to 10); 0 where e^-x overflows.
 __device__ __forceinline__ float fast_sigmoid(float x) {
-    return __fdividef(1.f, 1.f + __expf(-x));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-x)));
+    return r;
 }
 
 }  // namespace gdn
