@@ -85,21 +85,210 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
+// Elements c .. c + 3 of a row of k or q, widened; 0 from Dk on.
+template <bool VEC, typename T>
+__device__ __forceinline__ float4 load_key(const T *row, int c, int Dk, bool aligned) {
+    if (VEC && aligned) return c < Dk ? load4(row + c) : make_float4(0, 0, 0, 0);
+    return make_float4(c < Dk ? to_f32(row[c]) : 0.f, c + 1 < Dk ? to_f32(row[c + 1]) : 0.f,
+                       c + 2 < Dk ? to_f32(row[c + 2]) : 0.f, c + 3 < Dk ? to_f32(row[c + 3]) : 0.f);
+}
+
+__device__ __forceinline__ float2 lo2(const float4 &x) { return make_float2(x.x, x.y); }
+__device__ __forceinline__ float2 hi2(const float4 &x) { return make_float2(x.z, x.w); }
+
 // LW lanes share a row, V float4 each; R rows per lane group, so ROWS rows per warp.
 constexpr int R = 4;
 template <int LW> constexpr int kRows = R * (32 / LW);
 
+// acc[r] += s_r . k, acc[R + r] += s_r . q over this lane's elements.
+template <int V>
+__device__ __forceinline__ void row_dots(const float4 (&s)[R][V], const float4 (&k4)[V],
+                                         const float4 (&q4)[V], float (&x)[2 * R]) {
+    float2 x2[2 * R];
+#pragma unroll
+    for (int i = 0; i < 2 * R; ++i) x2[i] = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            x2[r] = __ffma2_rn(lo2(s[r][v]), lo2(k4[v]), x2[r]);
+            x2[r] = __ffma2_rn(hi2(s[r][v]), hi2(k4[v]), x2[r]);
+            x2[R + r] = __ffma2_rn(lo2(s[r][v]), lo2(q4[v]), x2[R + r]);
+            x2[R + r] = __ffma2_rn(hi2(s[r][v]), hi2(q4[v]), x2[R + r]);
+        }
+#pragma unroll
+    for (int i = 0; i < 2 * R; ++i) x[i] = x2[i].x + x2[i].y;
+}
+
+// s_r <- g s_r
+template <int V>
+__device__ __forceinline__ void scale_rows(float4 (&s)[R][V], float g) {
+    const float2 g2 = make_float2(g, g);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float2 lo = __fmul2_rn(lo2(s[r][v]), g2), hi = __fmul2_rn(hi2(s[r][v]), g2);
+            s[r][v] = make_float4(lo.x, lo.y, hi.x, hi.y);
+        }
+}
+// s_r <- s_r + u_r k
+template <int V>
+__device__ __forceinline__ void add_rows(float4 (&s)[R][V], const float (&u)[R],
+                                         const float4 (&k4)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float2 uu = make_float2(u[r], u[r]);
+            const float2 lo = __ffma2_rn(uu, lo2(k4[v]), lo2(s[r][v]));
+            const float2 hi = __ffma2_rn(uu, hi2(k4[v]), hi2(s[r][v]));
+            s[r][v] = make_float4(lo.x, lo.y, hi.x, hi.y);
+        }
+}
+
+// A warp's rows of the state from wrow on, zero from Dv on.
+template <int LW, int V, bool VEC>
+__device__ __forceinline__ void load_rows(const RunsArgs &a, const float *state, int wrow, int lane,
+                                          bool run, float4 (&s)[R][V]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int row = wrow + lane / LW * R + r;
+            s[r][v] = run && row < a.Dv ? load_state<VEC>(state + (long long)row * a.Dk,
+                                                          4 * (v * LW + lane % LW), a.Dk)
+                                        : make_float4(0, 0, 0, 0);
+        }
+}
+template <int LW, int V, bool VEC>
+__device__ __forceinline__ void store_rows(const RunsArgs &a, float *state, int wrow, int lane,
+                                           const float4 (&s)[R][V]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int row = wrow + lane / LW * R + r;
+            if (row < a.Dv)
+                store_state<VEC>(state + (long long)row * a.Dk, 4 * (v * LW + lane % LW), a.Dk,
+                                 s[r][v]);
+        }
+}
+
+// Whether an earlier sequence with tokens names this slot (seen by every lane that
+// calls with its own share of the sequences).
+__device__ __forceinline__ int slot_taken(const RunsArgs &a, int n, int slot, int from, int step) {
+    int taken = 0;
+    for (int i = from; i < n; i += step)
+        if (a.slots[i] == slot) taken |= !a.cu || a.cu[i] < a.cu[i + 1];
+    return taken;
+}
+
+// Runs of one token: every warp for itself, k, q and their norms in registers and no
+// barrier, so the pass is as good as its loads and stores of the state.
+template <typename T, int LW, int V, bool VEC>
+__device__ __forceinline__ void one_token(const RunsArgs &a, float *state, int n, int h, int t,
+                                          int slot, bool run, int row0, int tiles) {
+    constexpr int ROWS = kRows<LW>, NK = 2 * R > LW ? 2 * R / LW : 1;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+    const int sub = lane % LW;
+    const int hk = h / (a.Hv / a.Hk);
+    const T *kr = static_cast<const T *>(a.k) + t * a.k_stride + (long long)hk * a.Dk;
+    const T *qr = a.q ? static_cast<const T *>(a.q) + t * a.q_stride + (long long)hk * a.Dk : nullptr;
+    const T *vr = static_cast<const T *>(a.v) + t * a.v_stride + (long long)h * a.Dv;
+    T *op = a.o ? static_cast<T *>(a.o) + ((long long)t * a.Hv + h) * a.Dv : nullptr;
+    const bool rows_aligned = a.k_stride % 4 == 0 && a.q_stride % 4 == 0;
+
+    float4 s[R][V], k4[V], q4[V];
+    load_rows<LW, V, VEC>(a, state, row0 + warp * ROWS, lane, run, s);
+    float g0 = 0.f, g1 = 0.f;
+    if (run) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            k4[v] = load_key<VEC>(kr, 4 * (v * LW + sub), a.Dk, rows_aligned);
+            q4[v] = qr ? load_key<VEC>(qr, 4 * (v * LW + sub), a.Dk, rows_aligned)
+                       : make_float4(0, 0, 0, 0);
+        }
+        g0 = a.log_alpha[t * a.la_stride + h];
+        g1 = a.beta[t * a.be_stride + h];
+        if (a.update && a.slots &&
+            __any_sync(0xffffffffu, slot_taken(a, n, slot, lane, 32)))
+            run = false;
+    }
+    if (!run) {  // a row of padding: its outputs are zero, nothing else is touched
+        if (op)
+            for (int i = threadIdx.x; i < tiles * warps * ROWS && row0 + i < a.Dv; i += blockDim.x)
+                op[row0 + i] = from_f32<T>(0.f);
+        return;
+    }
+    float kk = 0.f, qq = 0.f, kq = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        kk += k4[v].x * k4[v].x + k4[v].y * k4[v].y + k4[v].z * k4[v].z + k4[v].w * k4[v].w;
+        qq += q4[v].x * q4[v].x + q4[v].y * q4[v].y + q4[v].z * q4[v].z + q4[v].w * q4[v].w;
+        kq += k4[v].x * q4[v].x + k4[v].y * q4[v].y + k4[v].z * q4[v].z + k4[v].w * q4[v].w;
+    }
+#pragma unroll
+    for (int off = LW / 2; off > 0; off >>= 1) {
+        kk += __shfl_xor_sync(0xffffffffu, kk, off);
+        qq += __shfl_xor_sync(0xffffffffu, qq, off);
+        kq += __shfl_xor_sync(0xffffffffu, kq, off);
+    }
+    const bool unit = a.flags & kFlagL2Norm;
+    const float rk = unit ? rsqrtf(kk + kNormEps) : 1.f, rq = unit ? rsqrtf(qq + kNormEps) : 1.f;
+    const float2 gp = gate_pair(g0, g1, a.flags);
+    const float alpha = expf(gp.x), beta = gp.y;
+    for (int tile = 0; tile < tiles; ++tile) {
+        const int wrow = row0 + (tile * warps + warp) * ROWS;
+        if (wrow >= a.Dv) return;
+        if (tile) load_rows<LW, V, VEC>(a, state, wrow, lane, true, s);
+        // a lane ends up with NK of the sums: rows' a in the lower half of its group,
+        // their b in the upper half; the lower half forms u and hands it over
+        const int grow = wrow + lane / LW * R;  // the lane group's first row
+        const int first = LW >= 2 * R ? sub / (LW / (2 * R)) : sub * NK;
+        float vv[NK];
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            const int row = grow + (first + i) % R;
+            vv[i] = row < a.Dv ? to_f32(vr[row]) : 0.f;
+        }
+        float x[2 * R];
+        row_dots<V>(s, k4, q4, x);
+        reduce_scatter<2 * R, LW>(x, lane);
+        float un[NK];
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            const float mine = beta * (vv[i] - alpha * rk * x[i]);  // meant in the lower half
+            un[i] = __shfl_sync(0xffffffffu, mine, lane % (LW / 2), LW);
+            const int row = grow + (first + i) % R;
+            if (op && first + i >= R && row < a.Dv)
+                op[row] = from_f32<T>(rq * (alpha * x[i] + un[i] * rk * kq));
+        }
+        if (!a.update) continue;
+        float u[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            u[r] = rk * __shfl_sync(0xffffffffu, un[r % NK], r / NK * (LW >= 2 * R ? LW / (2 * R) : 1),
+                                    LW);
+        scale_rows<V>(s, alpha);
+        add_rows<V>(s, u, k4);
+        store_rows<LW, V, VEC>(a, state, wrow, lane, s);
+    }
+}
+
+// A block: `tiles` times warps * ROWS value channels of one value head of one sequence.
 template <typename T, int LW, int V, bool VEC>
 __global__ void __launch_bounds__(32 * kMaxWarps, 3)
-decode_runs_kernel(RunsArgs a, int row_blocks) {
+decode_runs_kernel(RunsArgs a, int row_blocks, int tiles) {
     constexpr int ROWS = kRows<LW>;
     constexpr int PD = LW * V * 4;       // padded Dk
     constexpr int E = (PD + 31) / 32;    // a lane's elements of k where a warp holds a token
-    __shared__ __align__(16) float sk[kTok][PD], sq[kTok][PD], sv[kTok][kMaxWarps * ROWS];
+    __shared__ __align__(16) float sk[kTok][PD], sq[kTok][PD];
     // tm[0]: T with u = T r, tm[1]: M with o = gamma b + M r  (r = v - gamma a)
     __shared__ float sA[kTok][kTok], sP[kTok][kTok], tm[2][kTok][kTok];
     __shared__ float al[kTok], be[kTok], gam[kTok], tail[kTok];
-    __shared__ __align__(16) float ra[kMaxWarps][ROWS][kTok], rb_[kMaxWarps][ROWS][kTok];
+    // per warp and token, a row per column: a then r, b, the corrections
+    __shared__ __align__(16) float ra[kMaxWarps][kTok][ROWS], rb_[kMaxWarps][kTok][ROWS];
     __shared__ __align__(16) float su[kMaxWarps][kTok][ROWS];
 
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, warps = blockDim.x / 32;
@@ -110,266 +299,221 @@ decode_runs_kernel(RunsArgs a, int row_blocks) {
     const int slot = a.slots ? a.slots[n] : n;
     if (t0 < 0 || t1 > a.total || t0 >= t1) return;  // empty, or offsets that are none
     bool run = slot >= 0 && slot < a.n_slots;
-    const int row0 = rb * warps * ROWS;
-    const T *vp = static_cast<const T *>(a.v);
-    T *op = static_cast<T *>(a.o);
-
-    const int sub = lane % LW, grp = lane / LW;
-    const int wrow = row0 + warp * ROWS;  // the warp's first row
+    const int row0 = rb * tiles * warps * ROWS;
     float *state = a.states + ((long long)(run ? slot : 0) * a.Hv + h) * a.Dv * a.Dk;
-    float4 s[R][V];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int row = wrow + grp * R + r;
-            s[r][v] = run && row < a.Dv
-                          ? load_state<VEC>(state + (long long)row * a.Dk, 4 * (v * LW + sub), a.Dk)
-                          : make_float4(0, 0, 0, 0);
-        }
+    if (t1 - t0 == 1) {
+        one_token<T, LW, V, VEC>(a, state, n, h, t0, slot, run, row0, tiles);
+        return;
+    }
+    const T *vp = static_cast<const T *>(a.v) + (long long)h * a.Dv;
+    T *op = a.o ? static_cast<T *>(a.o) + (long long)h * a.Dv : nullptr;
+    const int sub = lane % LW, grp = lane / LW;
     const int hk = h / (a.Hv / a.Hk);
+    float4 s[R][V];
+    load_rows<LW, V, VEC>(a, state, row0 + warp * ROWS, lane, run, s);
 
-    for (int c0 = t0; c0 < t1; c0 += kTok) {
-        const int m = min(kTok, t1 - c0);
-        // a warp per token: k and q (normalised), v of the block's rows, the gates
-        for (int j = warp; j < m && run; j += warps) {
-            const long long t = c0 + j;
-            const T *kr = static_cast<const T *>(a.k) + t * a.k_stride + (long long)hk * a.Dk;
-            const T *qr = a.q ? static_cast<const T *>(a.q) + t * a.q_stride + (long long)hk * a.Dk
-                              : nullptr;
-            const T *vr = vp + t * a.v_stride + (long long)h * a.Dv;
-            float x[E], y[E];
+    for (int tile = 0; tile < tiles; ++tile) {
+        const int wrow = row0 + (tile * warps + warp) * ROWS;  // the warp's first row
+        if (row0 + tile * warps * ROWS >= a.Dv) break;
+        if (tile) load_rows<LW, V, VEC>(a, state, wrow, lane, true, s);
+        for (int c0 = t0; c0 < t1; c0 += kTok) {
+            const int m = min(kTok, t1 - c0);
+            // a run of one chunk keeps its tokens' arrays for all row tiles
+            if (tile == 0 || t1 - t0 > kTok) {
+                if (tile || c0 > t0) __syncthreads();  // the arrays are written again
+                // a warp per token: k and q (normalised), the gates
+                for (int j = warp; j < m && run; j += warps) {
+                    const long long t = c0 + j;
+                    const T *kr = static_cast<const T *>(a.k) + t * a.k_stride + (long long)hk * a.Dk;
+                    const T *qr = a.q ? static_cast<const T *>(a.q) + t * a.q_stride +
+                                            (long long)hk * a.Dk
+                                      : nullptr;
+                    float x[E], y[E];
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const int c = lane + 32 * i;
-                x[i] = c < a.Dk ? to_f32(kr[c]) : 0.f;
-                y[i] = qr && c < a.Dk ? to_f32(qr[c]) : 0.f;
-            }
-            const float g0 = a.log_alpha[t * a.la_stride + h], g1 = a.beta[t * a.be_stride + h];
-            for (int i = lane; i < warps * ROWS; i += 32)
-                sv[j][i] = row0 + i < a.Dv ? to_f32(vr[row0 + i]) : 0.f;
-            float kn = 0.f, qn = 0.f, kq = 0.f;
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                kn += x[i] * x[i];
-                qn += y[i] * y[i];
-                kq += x[i] * y[i];
-            }
-            float rk = 1.f, rq = 1.f;
-            if (a.flags & kFlagL2Norm) {
-                rk = rsqrtf(warp_sum(kn) + kNormEps);
-                rq = rsqrtf(warp_sum(qn) + kNormEps);
-            }
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const int c = lane + 32 * i;
-                if (c < PD) {
-                    sk[j][c] = rk * x[i];
-                    sq[j][c] = rq * y[i];
-                }
-            }
-            if (m == 1) kq = warp_sum(kq);
-            if (lane == 0) {
-                const float2 gp = gate_pair(g0, g1, a.flags);
-                const float alpha = expf(gp.x);
-                al[j] = alpha;
-                be[j] = gp.y;
-                if (m == 1) {
-                    gam[0] = alpha;
-                    tail[0] = 1.f;
-                    tm[0][0][0] = gp.y;
-                    tm[1][0][0] = gp.y * (rk * rq * kq);
-                }
-            }
-        }
-        if (c0 == t0) {
-            // of the sequences with tokens that name one slot the first has it
-            int taken = 0;
-            if (run && a.update && a.slots)
-                for (int i = tid; i < n; i += blockDim.x)
-                    if (a.slots[i] == slot) taken |= !a.cu || a.cu[i] < a.cu[i + 1];
-            if (__syncthreads_or(taken)) run = false;
-            if (!run) {  // a row of padding: its outputs are zero, nothing else is touched
-                if (op)
-                    for (int t = t0; t < t1; ++t)
-                        for (int i = tid; i < warps * ROWS && row0 + i < a.Dv; i += blockDim.x)
-                            op[((long long)t * a.Hv + h) * a.Dv + row0 + i] = from_f32<T>(0.f);
-                return;
-            }
-        } else {
-            __syncthreads();
-        }
-        if (m > 1) {
-            // a warp per token i: A_ij = beta_i Gamma_ij k_i.k_j (j < i) and
-            // P_ij = Gamma_ij q_i.k_j (j <= i)
-            for (int i = warp; i < m; i += warps) {
-                float x[2 * kTok];
-#pragma unroll
-                for (int j = 0; j < 2 * kTok; ++j) x[j] = 0.f;
-#pragma unroll
-                for (int c = 0; c < E; ++c) {
-                    const int at = lane + 32 * c;
-                    if (at < PD) {
-                        const float ki = sk[i][at], qi = sq[i][at];
-#pragma unroll
-                        for (int j = 0; j < kTok; ++j)
-                            if (j <= i) {
-                                const float kj = sk[j][at];
-                                x[j] += ki * kj;
-                                x[kTok + j] += qi * kj;
-                            }
+                    for (int i = 0; i < E; ++i) {
+                        const int c = lane + 32 * i;
+                        x[i] = c < a.Dk ? to_f32(kr[c]) : 0.f;
+                        y[i] = qr && c < a.Dk ? to_f32(qr[c]) : 0.f;
                     }
-                }
-                const int w = reduce_scatter<2 * kTok, 32>(x, lane), j = w % kTok;
-                float dec = 1.f;
-                for (int l = j + 1; l <= i; ++l) dec *= al[l];
-                if (lane % 2 == 0 && j <= i) {
-                    if (w < kTok) sA[i][j] = be[i] * dec * x[0];
-                    else sP[i][j] = dec * x[0];
-                }
-                if (lane == 0) {
-                    float g = 1.f;
-                    for (int l = 0; l <= i; ++l) g *= al[l];
-                    gam[i] = g;
-                    g = 1.f;
-                    for (int l = i + 1; l < m; ++l) g *= al[l];
-                    tail[i] = g;
-                }
-            }
-            __syncthreads();
-            if (warp == 0) {  // column j of T = (I + A)^-1 diag(beta), then of M = P T
-                const int j = lane % kTok;
-                float x[kTok];
+                    const float g0 = a.log_alpha[t * a.la_stride + h];
+                    const float g1 = a.beta[t * a.be_stride + h];
+                    float rk = 1.f, rq = 1.f;
+                    if (a.flags & kFlagL2Norm) {
+                        float kn = 0.f, qn = 0.f;
 #pragma unroll
-                for (int i = 0; i < kTok; ++i) {
-                    x[i] = i == j ? 1.f : 0.f;
-#pragma unroll
-                    for (int l = 0; l < i; ++l)
-                        if (i < m && l >= j) x[i] -= sA[i][l] * x[l];
-                }
-                const float b = j < m ? be[j] : 0.f;
-                for (int i = lane / kTok; i < m; i += 32 / kTok) {
-                    float p = 0.f, xi = 0.f;
-#pragma unroll
-                    for (int l = 0; l < kTok; ++l)
-                        if (l >= j && l <= i) {
-                            p += sP[i][l] * x[l];
-                            if (l == i) xi = x[l];
+                        for (int i = 0; i < E; ++i) {
+                            kn += x[i] * x[i];
+                            qn += y[i] * y[i];
                         }
-                    if (j <= i) {
-                        tm[0][i][j] = b * xi;
-                        tm[1][i][j] = b * p;
+                        rk = rsqrtf(warp_sum(kn) + kNormEps);
+                        rq = rsqrtf(warp_sum(qn) + kNormEps);
+                    }
+#pragma unroll
+                    for (int i = 0; i < E; ++i) {
+                        const int c = lane + 32 * i;
+                        if (c < PD) {
+                            sk[j][c] = rk * x[i];
+                            sq[j][c] = rq * y[i];
+                        }
+                    }
+                    if (lane == 0) {
+                        const float2 gp = gate_pair(g0, g1, a.flags);
+                        al[j] = expf(gp.x);
+                        be[j] = gp.y;
+                    }
+                }
+                if (tile == 0 && c0 == t0) {
+                    // of the sequences with tokens that name one slot the first has it
+                    const int taken = run && a.update && a.slots
+                                          ? slot_taken(a, n, slot, tid, blockDim.x) : 0;
+                    if (__syncthreads_or(taken)) run = false;
+                    if (!run) {  // a row of padding: its outputs are zero, nothing else is touched
+                        if (op)
+                            for (int t = t0; t < t1; ++t)
+                                for (int i = tid; i < tiles * warps * ROWS && row0 + i < a.Dv;
+                                     i += blockDim.x)
+                                    op[(long long)t * a.Hv * a.Dv + row0 + i] = from_f32<T>(0.f);
+                        return;
+                    }
+                } else {
+                    __syncthreads();
+                }
+                // a warp per token i: A_ij = beta_i Gamma_ij k_i.k_j (j < i) and
+                // P_ij = Gamma_ij q_i.k_j (j <= i)
+                for (int i = warp; i < m; i += warps) {
+                    float x[2 * kTok];
+#pragma unroll
+                    for (int j = 0; j < 2 * kTok; ++j) x[j] = 0.f;
+#pragma unroll
+                    for (int c = 0; c < E; ++c) {
+                        const int at = lane + 32 * c;
+                        if (at < PD) {
+                            const float ki = sk[i][at], qi = sq[i][at];
+#pragma unroll
+                            for (int j = 0; j < kTok; ++j)
+                                if (j <= i) {
+                                    const float kj = sk[j][at];
+                                    x[j] += ki * kj;
+                                    x[kTok + j] += qi * kj;
+                                }
+                        }
+                    }
+                    const int w = reduce_scatter<2 * kTok, 32>(x, lane), j = w % kTok;
+                    float dec = 1.f;
+                    for (int l = j + 1; l <= i; ++l) dec *= al[l];
+                    if (lane % 2 == 0 && j <= i) {
+                        if (w < kTok) sA[i][j] = be[i] * dec * x[0];
+                        else sP[i][j] = dec * x[0];
+                    }
+                    if (lane == 0) {
+                        float g = 1.f;
+                        for (int l = 0; l <= i; ++l) g *= al[l];
+                        gam[i] = g;
+                        g = 1.f;
+                        for (int l = i + 1; l < m; ++l) g *= al[l];
+                        tail[i] = g;
+                    }
+                }
+                __syncthreads();
+                if (warp == 0) {  // column j of T = (I + A)^-1 diag(beta), then of M = P T
+                    const int j = lane % kTok;
+                    float x[kTok];
+#pragma unroll
+                    for (int i = 0; i < kTok; ++i) {
+                        x[i] = i == j ? 1.f : 0.f;
+#pragma unroll
+                        for (int l = 0; l < i; ++l)
+                            if (i < m && l >= j) x[i] -= sA[i][l] * x[l];
+                    }
+                    const float b = j < m ? be[j] : 0.f;
+                    for (int i = lane / kTok; i < m; i += 32 / kTok) {
+                        float p = 0.f, xi = 0.f;
+#pragma unroll
+                        for (int l = 0; l < kTok; ++l)
+                            if (l >= j && l <= i) {
+                                p += sP[i][l] * x[l];
+                                if (l == i) xi = x[l];
+                            }
+                        if (j <= i) {
+                            tm[0][i][j] = b * xi;
+                            tm[1][i][j] = b * p;
+                        }
                     }
                 }
             }
-        }
-        // the rows' products with k and q
-        for (int j = 0; j < m; ++j) {
-            float2 x2[2 * R];
+            // the rows' products with k and q
+            for (int j = 0; j < m; ++j) {
+                float4 k4[V], q4[V];
 #pragma unroll
-            for (int i = 0; i < 2 * R; ++i) x2[i] = make_float2(0.f, 0.f);
+                for (int v = 0; v < V; ++v) {
+                    k4[v] = *reinterpret_cast<const float4 *>(&sk[j][4 * (v * LW + sub)]);
+                    q4[v] = *reinterpret_cast<const float4 *>(&sq[j][4 * (v * LW + sub)]);
+                }
+                float x[2 * R];
+                row_dots<V>(s, k4, q4, x);
+                const int first = reduce_scatter<2 * R, LW>(x, lane);
+                constexpr int NK = 2 * R > LW ? 2 * R / LW : 1;  // sums left in a lane
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float4 k4 = *reinterpret_cast<const float4 *>(&sk[j][4 * (v * LW + sub)]);
-                const float4 q4 = *reinterpret_cast<const float4 *>(&sq[j][4 * (v * LW + sub)]);
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const float2 lo = make_float2(s[r][v].x, s[r][v].y);
-                    const float2 hi = make_float2(s[r][v].z, s[r][v].w);
-                    x2[r] = __ffma2_rn(lo, make_float2(k4.x, k4.y), x2[r]);
-                    x2[r] = __ffma2_rn(hi, make_float2(k4.z, k4.w), x2[r]);
-                    x2[R + r] = __ffma2_rn(lo, make_float2(q4.x, q4.y), x2[R + r]);
-                    x2[R + r] = __ffma2_rn(hi, make_float2(q4.z, q4.w), x2[R + r]);
+                for (int i = 0; i < NK; ++i) {
+                    const int w = first + i;
+                    (w < R ? ra[warp][j][grp * R + w] : rb_[warp][j][grp * R + w - R]) = x[i];
                 }
             }
-            float x[2 * R];
-#pragma unroll
-            for (int i = 0; i < 2 * R; ++i) x[i] = x2[i].x + x2[i].y;
-            const int first = reduce_scatter<2 * R, LW>(x, lane);
-            constexpr int NK = 2 * R > LW ? 2 * R / LW : 1;  // sums left in a lane
-#pragma unroll
-            for (int i = 0; i < NK; ++i) {
-                const int w = first + i;
-                (w < R ? ra[warp][grp * R + w][j] : rb_[warp][grp * R + w - R][j]) = x[i];
+            if (tile == 0 || t1 - t0 > kTok) __syncthreads();  // T and M are there
+            else __syncwarp();
+            // each row's r, then its outputs and corrections
+            for (int at = lane; at < ROWS * m; at += 32) {
+                const int j = at / ROWS, row = at % ROWS;
+                const float v = wrow + row < a.Dv ? to_f32(vp[(c0 + j) * a.v_stride + wrow + row]) : 0.f;
+                ra[warp][j][row] = v - gam[j] * ra[warp][j][row];
             }
-        }
-        if (m > 1) __syncthreads();
-        else __syncwarp();
-        // each row's r, then its outputs and corrections
-        for (int i = lane; i < ROWS * kTok; i += 32) {
-            const int row = i / kTok, j = i % kTok;
-            if (j < m) ra[warp][row][j] = sv[j][warp * ROWS + row] - gam[j] * ra[warp][row][j];
-        }
-        __syncwarp();
-        for (int at = lane; at < ROWS * kTok; at += 32) {
-            const int row = at / kTok, i = at % kTok;
-            if (i < m) {
-                float u = 0.f, out = gam[i] * rb_[warp][row][i];
-#pragma unroll
-                for (int j = 0; j < kTok; ++j)
-                    if (j <= i) {
-                        const float r = ra[warp][row][j];
-                        u += tm[0][i][j] * r;
-                        out += tm[1][i][j] * r;
-                    }
+            __syncwarp();
+            for (int at = lane; at < ROWS * m; at += 32) {
+                const int i = at / ROWS, row = at % ROWS;
+                float u = 0.f, out = gam[i] * rb_[warp][i][row];
+                for (int j = 0; j <= i; ++j) {
+                    const float r = ra[warp][j][row];
+                    u += tm[0][i][j] * r;
+                    out += tm[1][i][j] * r;
+                }
                 su[warp][i][row] = tail[i] * u;
                 if (op && wrow + row < a.Dv)
-                    op[((long long)(c0 + i) * a.Hv + h) * a.Dv + wrow + row] = from_f32<T>(out);
+                    op[(long long)(c0 + i) * a.Hv * a.Dv + wrow + row] = from_f32<T>(out);
             }
-        }
-        __syncwarp();
-        if (a.update || c0 + kTok < t1) {
-            const float g1 = gam[m - 1];
-            const float2 g = make_float2(g1, g1);
+            __syncwarp();
+            if (a.update || c0 + kTok < t1) {
+                scale_rows<V>(s, gam[m - 1]);
+                for (int j = 0; j < m; ++j) {
+                    const float4 u4 = *reinterpret_cast<const float4 *>(&su[warp][j][grp * R]);
+                    const float u[R] = {u4.x, u4.y, u4.z, u4.w};
+                    float4 k4[V];
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float2 lo = __fmul2_rn(make_float2(s[r][v].x, s[r][v].y), g);
-                    const float2 hi = __fmul2_rn(make_float2(s[r][v].z, s[r][v].w), g);
-                    s[r][v] = make_float4(lo.x, lo.y, hi.x, hi.y);
-                }
-            for (int j = 0; j < m; ++j) {
-                const float4 u4 = *reinterpret_cast<const float4 *>(&su[warp][j][grp * R]);
-                const float u[R] = {u4.x, u4.y, u4.z, u4.w};
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float4 k4 = *reinterpret_cast<const float4 *>(&sk[j][4 * (v * LW + sub)]);
-#pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const float2 uu = make_float2(u[r], u[r]);
-                        const float2 lo = __ffma2_rn(uu, make_float2(k4.x, k4.y),
-                                                     make_float2(s[r][v].x, s[r][v].y));
-                        const float2 hi = __ffma2_rn(uu, make_float2(k4.z, k4.w),
-                                                     make_float2(s[r][v].z, s[r][v].w));
-                        s[r][v] = make_float4(lo.x, lo.y, hi.x, hi.y);
-                    }
+                    for (int v = 0; v < V; ++v)
+                        k4[v] = *reinterpret_cast<const float4 *>(&sk[j][4 * (v * LW + sub)]);
+                    add_rows<V>(s, u, k4);
                 }
             }
+            __syncwarp();
         }
-        if (c0 + kTok < t1) __syncthreads();  // the tokens' shared arrays are written again
+        if (a.update) store_rows<LW, V, VEC>(a, state, wrow, lane, s);
     }
-    if (!a.update) return;
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int row = wrow + grp * R + r;
-            if (row < a.Dv)
-                store_state<VEC>(state + (long long)row * a.Dk, 4 * (v * LW + sub), a.Dk, s[r][v]);
-        }
 }
 
 template <typename T, int LW, int V>
 cudaError_t launch(const RunsArgs &a, cudaStream_t st) {
     constexpr int ROWS = kRows<LW>;
     const int warps = min(kMaxWarps, (a.Dv + ROWS - 1) / ROWS);
-    const int row_blocks = (a.Dv + warps * ROWS - 1) / (warps * ROWS);
+    int tiles = (a.Dv + warps * ROWS - 1) / (warps * ROWS), row_blocks = 1;
+    // few heads: their rows are shared out over more blocks, up to two per SM
+    while (tiles > 1 && (long long)a.N * a.Hv * row_blocks < 148 * 2) {
+        tiles = (tiles + 1) / 2;
+        row_blocks = (a.Dv + tiles * warps * ROWS - 1) / (tiles * warps * ROWS);
+    }
     const unsigned blocks = (unsigned)((long long)a.N * a.Hv * row_blocks);
     if (a.Dk % 4 == 0)
-        decode_runs_kernel<T, LW, V, true><<<blocks, 32 * warps, 0, st>>>(a, row_blocks);
+        decode_runs_kernel<T, LW, V, true><<<blocks, 32 * warps, 0, st>>>(a, row_blocks, tiles);
     else
-        decode_runs_kernel<T, LW, V, false><<<blocks, 32 * warps, 0, st>>>(a, row_blocks);
+        decode_runs_kernel<T, LW, V, false><<<blocks, 32 * warps, 0, st>>>(a, row_blocks, tiles);
     return cudaPeekAtLastError();
 }
 
