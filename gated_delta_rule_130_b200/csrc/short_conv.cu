@@ -103,6 +103,7 @@ conv_fwd(ConvArgs a, unsigned ctiles) {
     static_assert(NT <= kThreads, "a thread per token");
     __shared__ Token tok[NT];
     __shared__ int seq[NT];
+    __shared__ __align__(8) unsigned char flag[(NT + 7) / 8 * 8];  // tok[].flags, packed
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int c = (int)((blockIdx.x % ctiles * kThreads + tid) * VEC);
     const int t0 = (int)(blockIdx.x / ctiles * TT), t1 = min(t0 + TT, a.total);
@@ -166,6 +167,10 @@ conv_fwd(ConvArgs a, unsigned ctiles) {
         }
         __syncthreads();
     }
+    if (B == 8) {
+        if (tid < (NT + 7) / 8 * 8) flag[tid] = tid < NT ? tok[tid].flags : 0;
+        __syncthreads();
+    }
     if (!live) return;
     int count = t1 - t0;
 #pragma unroll
@@ -176,15 +181,54 @@ conv_fwd(ConvArgs a, unsigned ctiles) {
     T *y = static_cast<T *>(a.part[p]) + (cc - a.begin[p]) + t0 * a.part_stride[p];
     float w[W][VEC], b[VEC];
     load_weights<T, VEC, W>(a, cc, w, b);
+    const T *ahead = x + (long long)(t0 + B) * a.x_stride;  // the rows loaded next
     for (int i0 = 0; i0 < count; i0 += B) {
         Raw<T, VEC> next[B];
-        if (i0 + B < count) {
+        if (i0 + 2 * B <= TT && t0 + i0 + 2 * B <= t1) {
 #pragma unroll
-            for (int i = 0; i < B; ++i)
-                if (t0 + i0 + B + i <= far)
-                    next[i] = load_raw<T, VEC>(x + (t0 + i0 + B + i) * a.x_stride);
+            for (int i = 0; i < B; ++i) {
+                next[i] = load_raw<T, VEC>(ahead);
+                ahead += a.x_stride;
+            }
+        } else if (i0 + B < count) {
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                if (t0 + i0 + B + i <= far) next[i] = load_raw<T, VEC>(ahead);
+                ahead += a.x_stride;
+            }
         }
+        if (B == 8 && *reinterpret_cast<const unsigned long long *>(&flag[i0]) ==
+                          0x0101010101010101ull * kMine) {
+            // eight tokens inside one sequence: no case to tell apart
+            float in[W - 1 + B][VEC];
 #pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) in[j][e] = win[j][e];
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                widen(cur[i], in[W - 1 + i]);
+                float z[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) z[e] = b[e];
+#pragma unroll
+                for (int j = 0; j < W; ++j) fma_vec<VEC>(w[j], in[i + j], z);
+                if (a.silu) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) z[e] *= fast_sigmoid(z[e]);
+                }
+                store_vec(y, z);
+                y += a.part_stride[p];
+            }
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) win[j][e] = in[B + j][e];
+#pragma unroll
+            for (int i = 0; i < B; ++i) cur[i] = next[i];
+            continue;
+        }
+#pragma unroll 1
         for (int i = 0; i < B; ++i) {
             if (i0 + i < count) {
                 const int f = tok[i0 + i].flags;
@@ -206,7 +250,7 @@ conv_fwd(ConvArgs a, unsigned ctiles) {
                     }
                 }
                 float now[VEC], z[VEC];
-                widen(cur[i], now);
+                load_vec<T, VEC>(x + (long long)(t0 + i0 + i) * a.x_stride, now);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) z[e] = b[e];
 #pragma unroll
@@ -263,7 +307,7 @@ conv_bwd(ConvArgs a, unsigned ctiles, int tile) {
     constexpr int B = 4;  // rows loaded at once
     // of each token of the tile and behind it: how many inputs of its sequence lie
     // before it (W - 1 at most), -1 where it is in none
-    __shared__ signed char before[kMaxTile + W - 1];
+    __shared__ __align__(4) signed char before[kMaxTile + W - 1];
     const int lane = threadIdx.x % 32;
     const int c = (int)((blockIdx.x % ctiles * kThreads + threadIdx.x) * VEC);
     const int t0 = (int)(blockIdx.x / ctiles) * tile, t1 = min(t0 + tile, a.total);
@@ -301,12 +345,15 @@ conv_bwd(ConvArgs a, unsigned ctiles, int tile) {
             before[t - t0] = sp.start < sp.end ? min(t - sp.start, W - 1) : -1;
         }
     }
-    float w[W][VEC], b[VEC], dw[W][VEC], db[VEC], acc[W][VEC];
+    float w[W][VEC], b[VEC], dw[W][VEC], db[VEC], acc[W - 1][VEC];
     load_weights<T, VEC, W>(a, cc, w, b);
 #pragma unroll
     for (int j = 0; j < W; ++j)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[j][e] = dw[j][e] = 0.f;
+        for (int e = 0; e < VEC; ++e) {
+            if (j < W - 1) acc[j][e] = 0.f;
+            dw[j][e] = 0.f;
+        }
 #pragma unroll
     for (int e = 0; e < VEC; ++e) db[e] = 0.f;
     __syncthreads();
@@ -314,75 +361,128 @@ conv_bwd(ConvArgs a, unsigned ctiles, int tile) {
     // acc[j]: dx of token t - (W - 1) + j so far; it leaves with the last token that
     // reads the input
     T *dx = static_cast<T *>(a.dx) + cc + (t0 - (W - 1)) * (long long)a.C;
+    const T *xa = x + (long long)(t0 + B) * a.x_stride;  // the rows loaded next
+    const T *da = dy + (long long)(t0 + B) * dy_stride;
     for (int i0 = t0; i0 < t1 + W - 1; i0 += B) {
         Raw<T, VEC> nx[B], nd[B];
+        if (i0 + 2 * B <= stop) {
 #pragma unroll
-        for (int i = 0; i < B; ++i)
-            if (i0 + B + i < stop) {
-                nx[i] = load_raw<T, VEC>(x + (i0 + B + i) * a.x_stride);
-                nd[i] = load_raw<T, VEC>(dy + (i0 + B + i) * dy_stride);
+            for (int i = 0; i < B; ++i) {
+                nx[i] = load_raw<T, VEC>(xa);
+                nd[i] = load_raw<T, VEC>(da);
+                xa += a.x_stride;
+                da += dy_stride;
             }
+        } else {
 #pragma unroll
-        for (int i = 0; i < B; ++i) {
-            const int t = i0 + i;
-            const int have = t < stop ? before[t - t0] : -1;
-            if (have >= 0) {
-                float in[W][VEC], d[VEC];
-                widen(cx[i], in[W - 1]);
-                widen(cd[i], d);
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) in[j][e] = win[j][e];
-                if (have < W - 1) {  // near the sequence's first token
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e)
-                            if (W - 1 - j > have) in[j][e] = 0.f;
+            for (int i = 0; i < B; ++i) {
+                if (i0 + B + i < stop) {
+                    nx[i] = load_raw<T, VEC>(xa);
+                    nd[i] = load_raw<T, VEC>(da);
                 }
+                xa += a.x_stride;
+                da += dy_stride;
+            }
+        }
+        if (i0 >= t0 + W - 1 && i0 + B <= t1 &&
+            *reinterpret_cast<const unsigned *>(&before[i0 - t0]) == 0x01010101u * (W - 1)) {
+            // four tokens inside one sequence and the tile: no case to tell apart
+            float in[W - 1 + B][VEC], out[W - 1 + B][VEC];
+#pragma unroll
+            for (int j = 0; j < W - 1 + B; ++j)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    if (j < W - 1) in[j][e] = win[j][e];
+                    out[j][e] = j < W - 1 ? acc[j][e] : 0.f;
+                }
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                float d[VEC];
+                widen(cx[i], in[W - 1 + i]);
+                widen(cd[i], d);
                 if (a.silu) {
                     float z[VEC];
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) z[e] = b[e];
 #pragma unroll
-                    for (int j = 0; j < W; ++j) fma_vec<VEC>(w[j], in[j], z);
+                    for (int j = 0; j < W; ++j) fma_vec<VEC>(w[j], in[i + j], z);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
                         const float sig = fast_sigmoid(z[e]);
                         d[e] *= fmaf(sig, fmaf(-z[e], sig, z[e]), sig);
                     }
                 }
-                if (have < W - 1) {
 #pragma unroll
-                    for (int j = 0; j < W; ++j)
-                        if (W - 1 - j <= have) fma_vec<VEC>(w[j], d, acc[j]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < W; ++j) fma_vec<VEC>(w[j], d, acc[j]);
-                }
-                if (t < t1) {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) db[e] += d[e];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) fma_vec<VEC>(d, in[j], dw[j]);
+                for (int j = 0; j < W; ++j) {
+                    fma_vec<VEC>(w[j], d, out[i + j]);
+                    fma_vec<VEC>(d, in[i + j], dw[j]);
                 }
 #pragma unroll
-                for (int j = 0; j + 1 < W - 1; ++j)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) win[W - 2][e] = in[W - 1][e];
+                for (int e = 0; e < VEC; ++e) db[e] += d[e];
+                store_vec(dx, out[i]);
+                dx += a.C;
             }
-            const int done = t - (W - 1);
-            if (done >= t0 && done < t1) store_vec(dx, acc[0]);
-            dx += a.C;
 #pragma unroll
             for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) acc[j][e] = acc[j + 1][e];
+                for (int e = 0; e < VEC; ++e) {
+                    win[j][e] = in[B + j][e];
+                    acc[j][e] = out[B + j][e];
+                }
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < B; ++i) {
+                const int t = i0 + i;
+                const int have = t < stop ? before[t - t0] : -1;
+                float out[W][VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) acc[W - 1][e] = 0.f;
+                for (int j = 0; j < W; ++j)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) out[j][e] = j < W - 1 ? acc[j][e] : 0.f;
+                if (have >= 0) {
+                    float in[W][VEC], d[VEC], now[VEC];
+                    load_vec<T, VEC>(x + (long long)t * a.x_stride, now);
+                    load_vec<T, VEC>(dy + (long long)t * dy_stride, d);
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e)  // the sequence's own inputs only
+                            in[j][e] = W - 1 - j > have ? 0.f : j < W - 1 ? win[j][e] : now[e];
+                    if (a.silu) {
+                        float z[VEC];
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) z[e] = b[e];
+#pragma unroll
+                        for (int j = 0; j < W; ++j) fma_vec<VEC>(w[j], in[j], z);
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) {
+                            const float sig = fast_sigmoid(z[e]);
+                            d[e] *= fmaf(sig, fmaf(-z[e], sig, z[e]), sig);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        if (W - 1 - j <= have) fma_vec<VEC>(w[j], d, out[j]);
+                    if (t < t1) {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) db[e] += d[e];
+#pragma unroll
+                        for (int j = 0; j < W; ++j) fma_vec<VEC>(d, in[j], dw[j]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e)
+                            win[j][e] = j + 1 < W - 1 ? win[j + 1][e] : now[e];
+                }
+                const int done = t - (W - 1);
+                if (done >= t0 && done < t1) store_vec(dx, out[0]);
+                dx += a.C;
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) acc[j][e] = out[j + 1][e];
+            }
         }
 #pragma unroll
         for (int i = 0; i < B; ++i) {
