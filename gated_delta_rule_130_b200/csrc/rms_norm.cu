@@ -79,97 +79,142 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&x)[VEC], fl
     }
 }
 
-// Element offset of row r in a tensor with `stride` elements per token.
-__device__ __forceinline__ long long row_at(const NormArgs &a, int r, long long stride) {
-    return (long long)(r / a.H) * stride + (long long)(r % a.H) * a.D;
-}
+// Where row r begins: its token and its elements before it in the token.
+struct Row {
+    long long token, in;
+    __device__ __forceinline__ Row(const NormArgs &a, int r) : token(r), in(0) {
+        if (a.H > 1) {
+            token = (unsigned)r / (unsigned)a.H;
+            in = (long long)(r - (int)token * a.H) * a.D;
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ const T *of(const void *p, long long stride) const {
+        return static_cast<const T *>(p) + token * stride + in;
+    }
+};
+
+enum Quant { kNoQuant, kRowQuant, kGroupQuant };
 
 // A row in registers: D <= VEC * TPR * IT, D a multiple of VEC.
-template <typename T, int VEC, int TPR, int IT>
+template <typename T, int VEC, int TPR, int IT, int Q>
 __global__ void __launch_bounds__(TPR > 32 ? TPR : 256)
 rms_fwd(NormArgs a) {
     constexpr int RPB = TPR > 32 ? 1 : 256 / TPR;  // rows per block
     __shared__ float part[2][32];
     const int sub = threadIdx.x % TPR;
     const int r = blockIdx.x * RPB + threadIdx.x / TPR;
-    const bool live = r < a.rows;
-    const int row = live ? r : 0;
-    const T *x = static_cast<const T *>(a.x) + row_at(a, row, a.x_stride);
-    const T *res = a.residual ? static_cast<const T *>(a.residual) + row_at(a, row, a.res_stride)
-                              : nullptr;
-    const T *gate = a.gate ? static_cast<const T *>(a.gate) + row_at(a, row, a.gate_stride) : nullptr;
+    const int width = r < a.rows ? a.D : 0;  // 0: a row behind the last one
+    const int row = r < a.rows ? r : 0;
+    const Row at(a, row);
+    const T *x = at.of<T>(a.x, a.x_stride);
     const long long out = (long long)row * a.D;
 
-    float h[IT][VEC];
-    Raw<T, VEC> g[IT];
+    Raw<T, VEC> h[IT], g[IT];
+    {
+        Raw<T, VEC> b[IT];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int c = (i * TPR + sub) * VEC;
+            if (c < width) h[i] = load_raw<T, VEC>(x + c);
+        }
+        if (a.residual) {
+            const T *res = at.of<T>(a.residual, a.res_stride);
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const int c = (i * TPR + sub) * VEC;
+                if (c < width) b[i] = load_raw<T, VEC>(res + c);
+            }
+        }
+        if (a.gate) {
+            const T *gate = at.of<T>(a.gate, a.gate_stride);
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const int c = (i * TPR + sub) * VEC;
+                if (c < width) g[i] = load_raw<T, VEC>(gate + c);
+            }
+        }
+        if (a.residual) {
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const int c = (i * TPR + sub) * VEC;
+                float u[VEC], v[VEC];
+                widen(h[i], u);
+                widen(b[i], v);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) u[e] += v[e];
+                h[i] = pack(u, h[i]);
+                if (a.h && c < width)
+                    *reinterpret_cast<Raw<T, VEC> *>(static_cast<T *>(a.h) + out + c) = h[i];
+            }
+        } else if (a.h) {
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const int c = (i * TPR + sub) * VEC;
+                if (c < width)
+                    *reinterpret_cast<Raw<T, VEC> *>(static_cast<T *>(a.h) + out + c) = h[i];
+            }
+        }
+    }
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-        const int c = (i * TPR + sub) * VEC;
-        if (live && c < a.D) {
-            load_vec<T, VEC>(x + c, h[i]);
-            if (res) {
-                float b[VEC];
-                load_vec<T, VEC>(res + c, b);
+        float u[VEC], q[VEC] = {};
+        widen(h[i], u);
+        fma_vec<VEC>(u, u, q);
+        if ((i * TPR + sub) * VEC < width)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) h[i][e] = to_f32(from_f32<T>(h[i][e] + b[e]));
-            }
-            if (gate) g[i] = load_raw<T, VEC>(gate + c);
-        } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) h[i][e] = 0.f;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int c = (i * TPR + sub) * VEC;
-        if (a.h && live && c < a.D) store_vec(static_cast<T *>(a.h) + out + c, h[i]);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) ss += h[i][e] * h[i][e];
+            for (int e = 0; e < VEC; ++e) ss += q[e];
     }
     const float rstd = rsqrtf(row_reduce<TPR, false>(ss, part[0]) / a.D + a.eps);
-    float top = 0.f;
+    float y[Q == kRowQuant ? IT : 1][VEC], top = 0.f;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int c = (i * TPR + sub) * VEC;
-        if (live && c < a.D) {
+        float(&v)[VEC] = y[Q == kRowQuant ? i : 0];
+        if (c < width) {
             float w[VEC];
+            widen(h[i], v);
             load_param<T, VEC>(a.weight, c, a.weight_f32, w);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) h[i][e] *= rstd * w[e];
-            if (gate) {
+            for (int e = 0; e < VEC; ++e) v[e] *= rstd * w[e];
+            if (a.gate) {
                 float gg[VEC];
                 widen(g[i], gg);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) h[i][e] *= gg[e] * fast_sigmoid(gg[e]);
+                for (int e = 0; e < VEC; ++e) v[e] *= gg[e] * fast_sigmoid(gg[e]);
             }
-            if (!a.group) store_vec(static_cast<T *>(a.y) + out + c, h[i]);
-        }
-        if (a.group) {
-            float t = 0.f;
+        } else {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) t = max_nan(t, fabsf(h[i][e]));
-            if (a.group == a.D) {
-                top = max_nan(top, t);
-            } else {  // 128 columns: 128 / VEC neighbouring lanes (TPR is no smaller)
-                constexpr int LANES = 128 / VEC < TPR ? 128 / VEC : TPR;
-                float scale;
-                const float inv = quant_inverse(lanes_reduce<(LANES < 32 ? LANES : 32), true>(t), &scale);
-                if (live && c < a.D) {
-                    store_e4m3<VEC>(static_cast<uint8_t *>(a.y) + out + c, h[i], inv);
-                    if (c % 128 == 0) a.scale[(out + c) / 128] = scale;
-                }
+            for (int e = 0; e < VEC; ++e) v[e] = 0.f;
+        }
+        if (Q == kNoQuant) {
+            if (c < width) store_vec(static_cast<T *>(a.y) + out + c, v);
+            continue;
+        }
+        float t = 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) t = max_nan(t, fabsf(v[e]));
+        if (Q == kRowQuant) {
+            top = max_nan(top, t);
+        } else {  // 128 columns: 128 / VEC neighbouring lanes (TPR is no smaller)
+            constexpr int LANES = 128 / VEC < TPR ? 128 / VEC : TPR;
+            float scale;
+            const float inv = quant_inverse(lanes_reduce<(LANES < 32 ? LANES : 32), true>(t), &scale);
+            if (c < width) {
+                store_e4m3<VEC>(static_cast<uint8_t *>(a.y) + out + c, v, inv);
+                if (c % 128 == 0) a.scale[(out + c) / 128] = scale;
             }
         }
     }
-    if (a.group && a.group == a.D) {
+    if (Q == kRowQuant) {
         float scale;
         const float inv = quant_inverse(row_reduce<TPR, true>(top, part[1]), &scale);
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int c = (i * TPR + sub) * VEC;
-            if (live && c < a.D) {
-                store_e4m3<VEC>(static_cast<uint8_t *>(a.y) + out + c, h[i], inv);
+            if (c < width) {
+                store_e4m3<VEC>(static_cast<uint8_t *>(a.y) + out + c, y[Q == kRowQuant ? i : 0], inv);
                 if (c == 0) a.scale[row] = scale;
             }
         }
@@ -185,10 +230,10 @@ __global__ void __launch_bounds__(kAnyThreads)
 rms_fwd_any(NormArgs a) {
     __shared__ float part[2][32];
     const int row = blockIdx.x;
-    const T *x = static_cast<const T *>(a.x) + row_at(a, row, a.x_stride);
-    const T *res = a.residual ? static_cast<const T *>(a.residual) + row_at(a, row, a.res_stride)
-                              : nullptr;
-    const T *gate = a.gate ? static_cast<const T *>(a.gate) + row_at(a, row, a.gate_stride) : nullptr;
+    const Row at(a, row);
+    const T *x = at.of<T>(a.x, a.x_stride);
+    const T *res = a.residual ? at.of<T>(a.residual, a.res_stride) : nullptr;
+    const T *gate = a.gate ? at.of<T>(a.gate, a.gate_stride) : nullptr;
     const long long out = (long long)row * a.D;
     // h may take the place of x or of the residual, y that of x: once a.h is
     // written, h is read from there
@@ -244,8 +289,41 @@ rms_fwd_any(NormArgs a) {
 }
 
 // Backward, a row in registers; each block takes the rows blockIdx.x * RPB + ... in
-// steps of the grid, keeps its columns' sums for dw in registers and leaves them in
-// partial[blockIdx.x].
+// steps of the grid, the next row's loads being issued before this row's sums, keeps
+// its columns' sums for dw in registers and leaves them in partial[blockIdx.x].
+template <typename T, int VEC, int IT> struct RowRaw {
+    Raw<T, VEC> x[IT], dy[IT], g[IT], dr[IT];
+};
+template <typename T, int VEC, int TPR, int IT>
+__device__ __forceinline__ void load_row(const NormArgs &a, int r, int sub, RowRaw<T, VEC, IT> &v) {
+    const Row at(a, r);
+    const T *x = at.of<T>(a.x, a.x_stride), *dy = at.of<T>(a.dy, a.dy_stride);
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int c = (i * TPR + sub) * VEC;
+        if (c < a.D) {
+            v.x[i] = load_raw<T, VEC>(x + c);
+            v.dy[i] = load_raw<T, VEC>(dy + c);
+        }
+    }
+    if (a.gate) {
+        const T *gate = at.of<T>(a.gate, a.gate_stride);
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int c = (i * TPR + sub) * VEC;
+            if (c < a.D) v.g[i] = load_raw<T, VEC>(gate + c);
+        }
+    }
+    if (a.d_res) {
+        const T *dres = at.of<T>(a.d_res, a.dres_stride);
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int c = (i * TPR + sub) * VEC;
+            if (c < a.D) v.dr[i] = load_raw<T, VEC>(dres + c);
+        }
+    }
+}
+
 template <typename T, int VEC, int TPR, int IT>
 __global__ void __launch_bounds__(TPR > 32 ? TPR : 256)
 rms_bwd(NormArgs a) {
@@ -258,100 +336,95 @@ rms_bwd(NormArgs a) {
     for (int i = 0; i < IT; ++i)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) dw[i][e] = 0.f;
-    int turn = 0;
-    for (int r0 = blockIdx.x * RPB; r0 < a.rows; r0 += gridDim.x * RPB, turn ^= 1) {
-        const int r = r0 + threadIdx.x / TPR;
-        const bool live = r < a.rows;
-        const int row = live ? r : 0;
-        const T *x = static_cast<const T *>(a.x) + row_at(a, row, a.x_stride);
-        const T *dy = static_cast<const T *>(a.dy) + row_at(a, row, a.dy_stride);
-        const T *gate = a.gate ? static_cast<const T *>(a.gate) + row_at(a, row, a.gate_stride)
-                               : nullptr;
-        const T *dres = a.d_res ? static_cast<const T *>(a.d_res) + row_at(a, row, a.dres_stride)
-                                : nullptr;
-        const long long out = (long long)row * a.D;
-        float h[IT][VEC], d[IT][VEC];  // d: dn
-        Raw<T, VEC> g[IT], dr[IT];
-        float ss = 0.f, sd = 0.f;
+    const int step = gridDim.x * RPB;
+    int r = blockIdx.x * RPB + threadIdx.x / TPR, turn = 0;
+    RowRaw<T, VEC, IT> cur, next;
+    if (r < a.rows) load_row<T, VEC, TPR, IT>(a, r, sub, cur);
+    for (int r0 = blockIdx.x * RPB; r0 < a.rows; r0 += step, r += step, turn ^= 1) {
+        const int width = r < a.rows ? a.D : 0;
+        if (r < a.rows - step) load_row<T, VEC, TPR, IT>(a, r + step, sub, next);
+        const long long out = (long long)r * a.D;
+        float h[IT][VEC], t[IT][VEC], ss = 0.f, sd = 0.f;  // t: w dn
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int c = (i * TPR + sub) * VEC;
-            if (live && c < a.D) {
-                load_vec<T, VEC>(x + c, h[i]);
-                load_vec<T, VEC>(dy + c, d[i]);
-                if (gate) g[i] = load_raw<T, VEC>(gate + c);
-                if (dres) dr[i] = load_raw<T, VEC>(dres + c);
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) h[i][e] = d[i][e] = 0.f;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int c = (i * TPR + sub) * VEC;
-            if (live && c < a.D) {
-                float w[VEC];
+            if (c < width) {
+                float w[VEC], p[VEC] = {}, q[VEC] = {};
+                widen(cur.x[i], h[i]);
+                widen(cur.dy[i], t[i]);
                 load_param<T, VEC>(a.weight, c, a.weight_f32, w);
-                float gg[VEC];
-                if (gate) widen(g[i], gg);
+                if (a.gate) {
+                    float g[VEC];
+                    widen(cur.g[i], g);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) t[i][e] *= g[e] * fast_sigmoid(g[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) t[i][e] *= w[e];
+                fma_vec<VEC>(h[i], h[i], p);
+                fma_vec<VEC>(t[i], h[i], q);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    const float dn = gate ? d[i][e] * (gg[e] * fast_sigmoid(gg[e])) : d[i][e];
-                    ss += h[i][e] * h[i][e];
-                    sd += w[e] * dn * h[i][e];
+                    ss += p[e];
+                    sd += q[e];
                 }
             }
         }
-        if (TPR <= 32) {
-            ss = lanes_reduce<(TPR < 32 ? TPR : 32), false>(ss);
-            sd = lanes_reduce<(TPR < 32 ? TPR : 32), false>(sd);
-        } else {
-            ss = lanes_reduce<32, false>(ss);
-            sd = lanes_reduce<32, false>(sd);
+        ss = lanes_reduce<(TPR < 32 ? TPR : 32), false>(ss);
+        sd = lanes_reduce<(TPR < 32 ? TPR : 32), false>(sd);
+        if (TPR > 32) {
             if (threadIdx.x % 32 == 0) {
                 part[turn][threadIdx.x / 32][0] = ss;
                 part[turn][threadIdx.x / 32][1] = sd;
             }
             __syncthreads();  // two rows' parts in turn: one barrier per row is enough
             ss = sd = 0.f;
-            for (int i = 0; i < (int)blockDim.x / 32; ++i) {
+#pragma unroll
+            for (int i = 0; i < TPR / 32; ++i) {
                 ss += part[turn][i][0];
                 sd += part[turn][i][1];
             }
         }
         const float rstd = rsqrtf(ss / a.D + a.eps);
-        const float back = sd / a.D * rstd * rstd * rstd;
+        const float back = -(sd / a.D * rstd * rstd * rstd);
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int c = (i * TPR + sub) * VEC;
-            if (live && c < a.D) {
-                float w[VEC], gg[VEC], dx[VEC];
-                load_param<T, VEC>(a.weight, c, a.weight_f32, w);
-                if (gate) {
-                    widen(g[i], gg);
-                    float dg[VEC];
+            if (c < width) {
+                float dx[VEC], dn[VEC];
+                widen(cur.dy[i], dn);
+                if (a.gate) {
+                    float g[VEC], w[VEC], dg[VEC];
+                    widen(cur.g[i], g);
+                    load_param<T, VEC>(a.weight, c, a.weight_f32, w);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        const float sig = fast_sigmoid(gg[e]);
-                        dg[e] = d[i][e] * (h[i][e] * rstd) * w[e] * sig * (1.f + gg[e] * (1.f - sig));
-                        d[i][e] *= gg[e] * sig;
+                        const float sig = fast_sigmoid(g[e]);
+                        dg[e] = dn[e] * (h[i][e] * rstd) * w[e] * sig * (1.f + g[e] * (1.f - sig));
+                        dn[e] *= g[e] * sig;
                     }
                     store_vec(static_cast<T *>(a.dgate) + out + c, dg);
                 }
+                if (a.d_res) {
+                    widen(cur.dr[i], dx);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) dx[e] = 0.f;
+                }
+                float backs[VEC], rstds[VEC], n[VEC] = {};
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    dx[e] = rstd * (w[e] * d[i][e]) - h[i][e] * back;
-                    dw[i][e] += d[i][e] * (h[i][e] * rstd);
+                    backs[e] = back;
+                    rstds[e] = rstd;
                 }
-                if (dres) {
-                    float b[VEC];
-                    widen(dr[i], b);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) dx[e] += b[e];
-                }
+                fma_vec<VEC>(h[i], backs, dx);
+                fma_vec<VEC>(t[i], rstds, dx);
+                fma_vec<VEC>(h[i], rstds, n);
+                fma_vec<VEC>(dn, n, dw[i]);
                 store_vec(static_cast<T *>(a.dx) + out + c, dx);
             }
         }
+        cur = next;
     }
     float *mine = a.partial + (long long)blockIdx.x * a.D;
     if (TPR > 32) {
@@ -386,12 +459,10 @@ rms_bwd_any(NormArgs a) {
     float *mine = a.partial + (long long)blockIdx.x * a.D;
     for (int c = threadIdx.x; c < a.D; c += kAnyThreads) mine[c] = 0.f;
     for (int row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const T *x = static_cast<const T *>(a.x) + row_at(a, row, a.x_stride);
-        const T *dy = static_cast<const T *>(a.dy) + row_at(a, row, a.dy_stride);
-        const T *gate = a.gate ? static_cast<const T *>(a.gate) + row_at(a, row, a.gate_stride)
-                               : nullptr;
-        const T *dres = a.d_res ? static_cast<const T *>(a.d_res) + row_at(a, row, a.dres_stride)
-                                : nullptr;
+        const Row at(a, row);
+        const T *x = at.of<T>(a.x, a.x_stride), *dy = at.of<T>(a.dy, a.dy_stride);
+        const T *gate = a.gate ? at.of<T>(a.gate, a.gate_stride) : nullptr;
+        const T *dres = a.d_res ? at.of<T>(a.d_res, a.dres_stride) : nullptr;
         const long long out = (long long)row * a.D;
         float ss = 0.f, sd = 0.f, w[1];
         for (int c = threadIdx.x; c < a.D; c += kAnyThreads) {
@@ -435,6 +506,7 @@ rms_bwd_sum(const float *partial, float *dw, int blocks, int D) {
     const int tx = threadIdx.x % 32, ty = threadIdx.x / 32, c = blockIdx.x * 32 + tx;
     float s = 0.f;
     if (c < D)
+#pragma unroll 8
         for (int b = ty; b < blocks; b += 32) s += partial[(long long)b * D + c];
     part[ty][tx] = s;
     __syncthreads();
@@ -457,7 +529,10 @@ bool vectors_fit(const NormArgs &a, int elem) {
 template <typename T, int VEC, int TPR, int IT>
 void run_fwd(const NormArgs &a, cudaStream_t st) {
     constexpr int rpb = TPR > 32 ? 1 : 256 / TPR, threads = TPR > 32 ? TPR : 256;
-    rms_fwd<T, VEC, TPR, IT><<<(a.rows + rpb - 1) / rpb, threads, 0, st>>>(a);
+    const int blocks = (a.rows + rpb - 1) / rpb;
+    if (!a.group) rms_fwd<T, VEC, TPR, IT, kNoQuant><<<blocks, threads, 0, st>>>(a);
+    else if (a.group == a.D) rms_fwd<T, VEC, TPR, IT, kRowQuant><<<blocks, threads, 0, st>>>(a);
+    else rms_fwd<T, VEC, TPR, IT, kGroupQuant><<<blocks, threads, 0, st>>>(a);
 }
 template <typename T, int VEC, int TPR, int IT>
 void run_bwd(const NormArgs &a, cudaStream_t st) {
@@ -467,6 +542,10 @@ void run_bwd(const NormArgs &a, cudaStream_t st) {
     rms_bwd<T, VEC, TPR, IT><<<blocks, threads, 0, st>>>(a);
     rms_bwd_sum<<<(a.D + 31) / 32, 1024, 0, st>>>(a.partial, a.dw, blocks, a.D);
 }
+
+// From this many rows on a warp takes a row of up to 256 vectors by itself; fewer rows
+// are shared by a block each, so that they still reach more SMs.
+constexpr int kManyRows = 148 * 8;
 
 template <typename T, int VEC>
 cudaError_t fwd_t(const NormArgs &a, cudaStream_t st) {
@@ -483,8 +562,10 @@ cudaError_t fwd_t(const NormArgs &a, cudaStream_t st) {
         run_fwd<T, VEC, 32, 1>(a, st);
     } else if (nv <= 64) {
         run_fwd<T, VEC, 32, 2>(a, st);
-    } else if (nv <= 128) {
+    } else if (nv <= 128 && a.rows >= kManyRows) {
         run_fwd<T, VEC, 32, 4>(a, st);
+    } else if (nv <= 256 && a.rows >= kManyRows) {
+        run_fwd<T, VEC, 32, 8>(a, st);
     } else if (nv <= 256) {
         run_fwd<T, VEC, 128, 2>(a, st);
     } else if (nv <= 512) {

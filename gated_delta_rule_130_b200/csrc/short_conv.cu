@@ -99,7 +99,7 @@ template <typename T, int VEC, int W, int TT>
 __global__ void __launch_bounds__(kThreads)
 conv_fwd(ConvArgs a, unsigned ctiles) {
     constexpr int NT = TT + W - 2;          // the tile and the tokens behind it
-    constexpr int B = NT < 8 ? NT : 8;      // rows loaded at once
+    constexpr int B = 8;                    // rows loaded at once
     static_assert(NT <= kThreads, "a thread per token");
     __shared__ Token tok[NT];
     __shared__ int seq[NT];
@@ -167,10 +167,8 @@ conv_fwd(ConvArgs a, unsigned ctiles) {
         }
         __syncthreads();
     }
-    if (B == 8) {
-        if (tid < (NT + 7) / 8 * 8) flag[tid] = tid < NT ? tok[tid].flags : 0;
-        __syncthreads();
-    }
+    if (tid < (NT + 7) / 8 * 8) flag[tid] = tid < NT ? tok[tid].flags : 0;
+    __syncthreads();
     if (!live) return;
     int count = t1 - t0;
 #pragma unroll
@@ -197,8 +195,8 @@ conv_fwd(ConvArgs a, unsigned ctiles) {
                 ahead += a.x_stride;
             }
         }
-        if (B == 8 && *reinterpret_cast<const unsigned long long *>(&flag[i0]) ==
-                          0x0101010101010101ull * kMine) {
+        if (*reinterpret_cast<const unsigned long long *>(&flag[i0]) ==
+            0x0101010101010101ull * kMine) {
             // eight tokens inside one sequence: no case to tell apart
             float in[W - 1 + B][VEC];
 #pragma unroll
@@ -294,6 +292,99 @@ conv_fwd(ConvArgs a, unsigned ctiles) {
         }
 #pragma unroll
         for (int i = 0; i < B; ++i) cur[i] = next[i];
+    }
+}
+
+// Forward of few tokens (a decode batch), where latency counts: a block takes
+// kThreads * VEC channels of one token t, each warp for itself and without a barrier.
+// The token that begins a sequence brings the sequence's next W - 2 tokens with it.
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(kThreads)
+conv_few(ConvArgs a, unsigned ctiles) {
+    const int lane = threadIdx.x % 32;
+    const int c = (int)((blockIdx.x % ctiles * kThreads + threadIdx.x) * VEC);
+    const int t = (int)(blockIdx.x / ctiles);
+    const bool live = c < a.C;
+    const int cc = live ? c : 0;
+    const T *x = static_cast<const T *>(a.x) + cc;
+    float now[VEC], w[W][VEC], b[VEC];
+    load_vec<T, VEC>(x + t * a.x_stride, now);
+    load_weights<T, VEC, W>(a, cc, w, b);
+
+    int n = t, start = t, end = t + 1;
+    if (a.cu) {
+        n = (int)((long long)t * a.N / a.total);  // where the sequences are equally long
+        start = a.cu[n];
+        end = a.cu[n + 1];
+        if (start > t || end <= t) {
+            n = seq_of(a.cu, a.N, t, lane);
+            start = a.cu[n];
+            end = a.cu[n + 1];
+        }
+        if (start < 0 || start > t || end <= t || end > a.total) return;  // in no sequence
+    }
+    const int pos = t - start;
+    if (pos > 0 && pos < W - 1) return;  // taken with the sequence's first token
+    int slot = -1;
+    if (a.states) {
+        slot = a.slots ? a.slots[n] : n;
+        if (slot >= a.n_slots) slot = -1;
+    }
+    const bool padding = a.states && slot < 0;
+    T *held = a.states && !padding
+                  ? static_cast<T *>(a.states) + (long long)slot * (W - 1) * a.C + cc : nullptr;
+    float win[W - 1][VEC];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+        if (pos) {
+            load_vec<T, VEC>(x + (t - (W - 1) + j) * a.x_stride, win[j]);
+        } else if (held) {
+            load_vec<T, VEC>(held + (long long)j * a.C, win[j]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) win[j][e] = 0.f;
+        }
+    }
+    // of the sequences with tokens that name one slot the first has it
+    bool zero = padding;
+    if (held && a.slots) {
+        int taken = 0;
+#pragma unroll 4
+        for (int k = lane; k < n; k += 32)
+            if (a.slots[k] == slot) taken |= !a.cu || a.cu[k] < a.cu[k + 1];
+        zero = __any_sync(0xffffffffu, taken);
+    }
+    if (!live) return;
+    const int p = part_of(a, cc);
+    T *y = static_cast<T *>(a.part[p]) + (cc - a.begin[p]) + t * a.part_stride[p];
+    const int last = pos ? t : min(t + W - 2, end - 1);
+    for (int s = t;; ++s) {
+        float z[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) z[e] = b[e];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) fma_vec<VEC>(w[j], win[j], z);
+        fma_vec<VEC>(w[W - 1], now, z);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            if (a.silu) z[e] *= fast_sigmoid(z[e]);
+            if (zero) z[e] = 0.f;
+        }
+        store_vec(y, z);
+        y += a.part_stride[p];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) win[j][e] = j + 1 < W - 1 ? win[j + 1][e] : now[e];
+        if (s == last) break;
+        load_vec<T, VEC>(x + (s + 1) * a.x_stride, now);
+    }
+    if (pos || !held || zero) return;
+    // the sequence's last inputs; win has them where it is that short
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+        if (end - start >= W - 1) load_vec<T, VEC>(x + (end - (W - 1) + j) * a.x_stride, win[j]);
+        store_vec(held + (long long)j * a.C, win[j]);
     }
 }
 
@@ -539,7 +630,7 @@ template <typename T, int VEC, int W>
 cudaError_t fwd_w(const ConvArgs &a, cudaStream_t st) {
     const unsigned ct = channel_tiles(a.C, VEC);
     if ((long long)ct * a.total <= 148 * 32) {
-        conv_fwd<T, VEC, W, 1><<<ct * a.total, kThreads, 0, st>>>(a, ct);
+        conv_few<T, VEC, W><<<ct * a.total, kThreads, 0, st>>>(a, ct);
     } else {
         conv_fwd<T, VEC, W, 32><<<ct * ((a.total + 31) / 32), kThreads, 0, st>>>(a, ct);
     }

@@ -95,11 +95,26 @@ __device__ __forceinline__ void fma_vec(const float (&x)[VEC], const float (&y)[
     }
 }
 
+// x packed to T, as one load would have brought it.
+__device__ __forceinline__ Raw<float, 4> pack(const float (&x)[4], Raw<float, 4>) {
+    return Raw<float, 4>{make_float4(x[0], x[1], x[2], x[3])};
+}
+__device__ __forceinline__ Raw<__nv_bfloat16, 8> pack(const float (&x)[8], Raw<__nv_bfloat16, 8>) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    return Raw<__nv_bfloat16, 8>{make_uint4(w[0], w[1], w[2], w[3])};
+}
+
 // 1 / (1 + e^-x) by the approximate power of two and reciprocal: off by at most a few
 // float32 roundings (1e-6 relative for |x| up to 10); 0 where e^-x overflows.
 __device__ __forceinline__ float fast_sigmoid(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-x)));
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
     return r;
 }
 
