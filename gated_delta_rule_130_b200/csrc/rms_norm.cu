@@ -291,6 +291,13 @@ rms_fwd_any(NormArgs a) {
 // Backward, a row in registers; each block takes the rows blockIdx.x * RPB + ... in
 // steps of the grid, the next row's loads being issued before this row's sums, keeps
 // its columns' sums for dw in registers and leaves them in partial[blockIdx.x].
+// The grid is the blocks that fit at once, 148 times this many (more than one round of
+// blocks leaves SMs idle in the last: 128 threads of 152 registers, 3 per SM with a
+// grid of 592, took 92.7 us on 16384 x 2048; 4 per SM of 128 registers 62.1 us).
+template <int TPR, int IT> constexpr int kBwdPerSM =
+    TPR > 256 ? 1 : TPR == 256 ? 2 : TPR == 128 ? (IT == 1 ? 6 : 4) : IT == 1 ? 3 : 2;
+constexpr int kMostBwdBlocks = 148 * 6;
+
 template <typename T, int VEC, int IT> struct RowRaw {
     Raw<T, VEC> x[IT], dy[IT], g[IT], dr[IT];
 };
@@ -325,7 +332,7 @@ __device__ __forceinline__ void load_row(const NormArgs &a, int r, int sub, RowR
 }
 
 template <typename T, int VEC, int TPR, int IT>
-__global__ void __launch_bounds__(TPR > 32 ? TPR : 256)
+__global__ void __launch_bounds__(TPR > 32 ? TPR : 256, kBwdPerSM<TPR, IT>)
 rms_bwd(NormArgs a) {
     constexpr int RPB = TPR > 32 ? 1 : 256 / TPR;
     __shared__ float part[2][32][2];
@@ -514,8 +521,8 @@ rms_bwd_sum(const float *partial, float *dw, int blocks, int D) {
     if (tx == 0 && blockIdx.x * 32 + ty < D) dw[blockIdx.x * 32 + ty] = s;
 }
 
-// Backward blocks: enough to fill 148 SMs a few times over.
-int bwd_blocks(int rows) { return rows < 592 ? rows : 592; }
+// Partial sums a workspace has room for.
+int bwd_blocks(int rows) { return rows < kMostBwdBlocks ? rows : kMostBwdBlocks; }
 
 bool aligned(const void *p, long long stride, int elem) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * elem % 16 == 0;
@@ -537,7 +544,7 @@ void run_fwd(const NormArgs &a, cudaStream_t st) {
 template <typename T, int VEC, int TPR, int IT>
 void run_bwd(const NormArgs &a, cudaStream_t st) {
     constexpr int rpb = TPR > 32 ? 1 : 256 / TPR, threads = TPR > 32 ? TPR : 256;
-    const int need = (a.rows + rpb - 1) / rpb, most = bwd_blocks(a.rows);
+    const int need = (a.rows + rpb - 1) / rpb, most = 148 * kBwdPerSM<TPR, IT>;
     const int blocks = need < most ? need : most;
     rms_bwd<T, VEC, TPR, IT><<<blocks, threads, 0, st>>>(a);
     rms_bwd_sum<<<(a.D + 31) / 32, 1024, 0, st>>>(a.partial, a.dw, blocks, a.D);

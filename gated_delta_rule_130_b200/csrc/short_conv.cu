@@ -95,12 +95,20 @@ struct __align__(16) Token {  // what a block knows of one of its tokens
     int flags, start, end, slot;
 };
 
-template <typename T, int VEC, int W, int TT>
+// All rows of the tile are on their way to shared memory at once, each thread's
+// own channels by itself, in groups of 8 rows.
+template <typename T, int VEC> constexpr int kTile = VEC * sizeof(T) > 8 ? 16 : 32;
+
+template <typename T, int VEC, int W>
 __global__ void __launch_bounds__(kThreads)
 conv_fwd(ConvArgs a, unsigned ctiles) {
+    constexpr int TT = kTile<T, VEC>;
     constexpr int NT = TT + W - 2;          // the tile and the tokens behind it
-    constexpr int B = 8;                    // rows loaded at once
+    constexpr int B = 8;                    // rows per group
+    constexpr int NG = (NT + B - 1) / B;
     static_assert(NT <= kThreads, "a thread per token");
+    static_assert(NG <= 5, "copy_wait's cases");
+    __shared__ __align__(16) Raw<T, VEC> rows[NT][kThreads];
     __shared__ Token tok[NT];
     __shared__ int seq[NT];
     __shared__ __align__(8) unsigned char flag[(NT + 7) / 8 * 8];  // tok[].flags, packed
@@ -112,18 +120,20 @@ conv_fwd(ConvArgs a, unsigned ctiles) {
     const int cc = live ? c : 0;
     const T *x = static_cast<const T *>(a.x) + cc;
 
-    // the inputs before the tile and its first rows are on their way while the
-    // sequences are found
-    Raw<T, VEC> cur[B];
-    float win[W - 1][VEC];
+    // the rows are on their way while the sequences are found
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+#pragma unroll
+        for (int i = g * B; i < g * B + B && i < NT; ++i)
+            if (t0 + i <= far) copy_async<T, VEC>(&rows[i][tid], x + (t0 + i) * a.x_stride);
+        copy_commit();
+    }
+    float win[W - 1][VEC];  // the inputs before the token
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
         const int s = t0 - (W - 1) + j;
         if (s >= 0) load_vec<T, VEC>(x + s * a.x_stride, win[j]);
     }
-#pragma unroll
-    for (int i = 0; i < B; ++i)
-        if (t0 + i <= far) cur[i] = load_raw<T, VEC>(x + (t0 + i) * a.x_stride);
 
     if (warp * 32 < NT) {
         int lo = 0, hi = 0;
@@ -179,21 +189,13 @@ conv_fwd(ConvArgs a, unsigned ctiles) {
     T *y = static_cast<T *>(a.part[p]) + (cc - a.begin[p]) + t0 * a.part_stride[p];
     float w[W][VEC], b[VEC];
     load_weights<T, VEC, W>(a, cc, w, b);
-    const T *ahead = x + (long long)(t0 + B) * a.x_stride;  // the rows loaded next
     for (int i0 = 0; i0 < count; i0 += B) {
-        Raw<T, VEC> next[B];
-        if (i0 + 2 * B <= TT && t0 + i0 + 2 * B <= t1) {
-#pragma unroll
-            for (int i = 0; i < B; ++i) {
-                next[i] = load_raw<T, VEC>(ahead);
-                ahead += a.x_stride;
-            }
-        } else if (i0 + B < count) {
-#pragma unroll
-            for (int i = 0; i < B; ++i) {
-                if (t0 + i0 + B + i <= far) next[i] = load_raw<T, VEC>(ahead);
-                ahead += a.x_stride;
-            }
+        switch (NG - 1 - i0 / B) {  // this group's rows have come
+            case 4: copy_wait<4>(); break;
+            case 3: copy_wait<3>(); break;
+            case 2: copy_wait<2>(); break;
+            case 1: copy_wait<1>(); break;
+            default: copy_wait<0>();
         }
         if (*reinterpret_cast<const unsigned long long *>(&flag[i0]) ==
             0x0101010101010101ull * kMine) {
@@ -205,7 +207,7 @@ conv_fwd(ConvArgs a, unsigned ctiles) {
                 for (int e = 0; e < VEC; ++e) in[j][e] = win[j][e];
 #pragma unroll
             for (int i = 0; i < B; ++i) {
-                widen(cur[i], in[W - 1 + i]);
+                widen(rows[i0 + i][tid], in[W - 1 + i]);
                 float z[VEC];
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) z[e] = b[e];
@@ -222,8 +224,6 @@ conv_fwd(ConvArgs a, unsigned ctiles) {
             for (int j = 0; j < W - 1; ++j)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) win[j][e] = in[B + j][e];
-#pragma unroll
-            for (int i = 0; i < B; ++i) cur[i] = next[i];
             continue;
         }
 #pragma unroll 1
@@ -248,7 +248,7 @@ conv_fwd(ConvArgs a, unsigned ctiles) {
                     }
                 }
                 float now[VEC], z[VEC];
-                load_vec<T, VEC>(x + (long long)(t0 + i0 + i) * a.x_stride, now);
+                widen(rows[i0 + i][tid], now);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) z[e] = b[e];
 #pragma unroll
@@ -290,8 +290,6 @@ conv_fwd(ConvArgs a, unsigned ctiles) {
                 }
             }
         }
-#pragma unroll
-        for (int i = 0; i < B; ++i) cur[i] = next[i];
     }
 }
 
@@ -389,13 +387,19 @@ conv_few(ConvArgs a, unsigned ctiles) {
 }
 
 constexpr int kMaxTile = 1024;  // tokens per block of the backward
+// Its blocks per SM: 5 of 102 registers a thread.
+template <typename T, int VEC> constexpr int kBwdPerSM = VEC * sizeof(T) > 8 ? 4 : 5;
 
 // Backward.  A block: kThreads * VEC channels and the tokens [t0, t0 + tile): their dx
 // (dz of the W - 1 tokens behind the tile is formed again) and their share of dw.
+// The rows of x and dy come through a ring of shared memory, each thread's own
+// channels by itself, S - 1 groups of B rows ahead.
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBwdPerSM<T, VEC>)
 conv_bwd(ConvArgs a, unsigned ctiles, int tile) {
-    constexpr int B = 4;  // rows loaded at once
+    constexpr int B = 4, S = VEC * sizeof(T) > 8 ? 2 : 4;
+    __shared__ __align__(16) Raw<T, VEC> ring[2][S][B][kThreads];
+    const int tid = threadIdx.x;
     // of each token of the tile and behind it: how many inputs of its sequence lie
     // before it (W - 1 at most), -1 where it is in none
     __shared__ __align__(4) signed char before[kMaxTile + W - 1];
@@ -418,13 +422,24 @@ conv_bwd(ConvArgs a, unsigned ctiles, int tile) {
         for (int e = 0; e < VEC; ++e) win[j][e] = 0.f;
         if (s >= 0) load_vec<T, VEC>(x + s * a.x_stride, win[j]);
     }
-    Raw<T, VEC> cx[B], cd[B];
+    const T *xa = x + (long long)t0 * a.x_stride;  // the rows copied next
+    const T *da = dy + (long long)t0 * dy_stride;
+    int copied = t0;
+    const auto copy_group = [&](int slot) {
 #pragma unroll
-    for (int i = 0; i < B; ++i)
-        if (t0 + i < stop) {
-            cx[i] = load_raw<T, VEC>(x + (t0 + i) * a.x_stride);
-            cd[i] = load_raw<T, VEC>(dy + (t0 + i) * dy_stride);
+        for (int i = 0; i < B; ++i) {
+            if (copied + i < stop) {
+                copy_async<T, VEC>(&ring[0][slot][i][tid], xa);
+                copy_async<T, VEC>(&ring[1][slot][i][tid], da);
+            }
+            xa += a.x_stride;
+            da += dy_stride;
         }
+        copied += B;
+        copy_commit();
+    };
+#pragma unroll
+    for (int g = 0; g < S - 1; ++g) copy_group(g);
     {
         int lo = 0, hi = 0;
         if (a.cu) {
@@ -452,29 +467,10 @@ conv_bwd(ConvArgs a, unsigned ctiles, int tile) {
     // acc[j]: dx of token t - (W - 1) + j so far; it leaves with the last token that
     // reads the input
     T *dx = static_cast<T *>(a.dx) + cc + (t0 - (W - 1)) * (long long)a.C;
-    const T *xa = x + (long long)(t0 + B) * a.x_stride;  // the rows loaded next
-    const T *da = dy + (long long)(t0 + B) * dy_stride;
-    for (int i0 = t0; i0 < t1 + W - 1; i0 += B) {
-        Raw<T, VEC> nx[B], nd[B];
-        if (i0 + 2 * B <= stop) {
-#pragma unroll
-            for (int i = 0; i < B; ++i) {
-                nx[i] = load_raw<T, VEC>(xa);
-                nd[i] = load_raw<T, VEC>(da);
-                xa += a.x_stride;
-                da += dy_stride;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < B; ++i) {
-                if (i0 + B + i < stop) {
-                    nx[i] = load_raw<T, VEC>(xa);
-                    nd[i] = load_raw<T, VEC>(da);
-                }
-                xa += a.x_stride;
-                da += dy_stride;
-            }
-        }
+    int slot = 0;
+    for (int i0 = t0; i0 < t1 + W - 1; i0 += B, slot = slot + 1 == S ? 0 : slot + 1) {
+        copy_wait<S - 2>();  // this group's rows have come
+        copy_group(slot ? slot - 1 : S - 1);
         if (i0 >= t0 + W - 1 && i0 + B <= t1 &&
             *reinterpret_cast<const unsigned *>(&before[i0 - t0]) == 0x01010101u * (W - 1)) {
             // four tokens inside one sequence and the tile: no case to tell apart
@@ -489,8 +485,8 @@ conv_bwd(ConvArgs a, unsigned ctiles, int tile) {
 #pragma unroll
             for (int i = 0; i < B; ++i) {
                 float d[VEC];
-                widen(cx[i], in[W - 1 + i]);
-                widen(cd[i], d);
+                widen(ring[0][slot][i][tid], in[W - 1 + i]);
+                widen(ring[1][slot][i][tid], d);
                 if (a.silu) {
                     float z[VEC];
 #pragma unroll
@@ -532,8 +528,8 @@ conv_bwd(ConvArgs a, unsigned ctiles, int tile) {
                     for (int e = 0; e < VEC; ++e) out[j][e] = j < W - 1 ? acc[j][e] : 0.f;
                 if (have >= 0) {
                     float in[W][VEC], d[VEC], now[VEC];
-                    load_vec<T, VEC>(x + (long long)t * a.x_stride, now);
-                    load_vec<T, VEC>(dy + (long long)t * dy_stride, d);
+                    widen(ring[0][slot][i][tid], now);
+                    widen(ring[1][slot][i][tid], d);
 #pragma unroll
                     for (int j = 0; j < W; ++j)
 #pragma unroll
@@ -574,11 +570,6 @@ conv_bwd(ConvArgs a, unsigned ctiles, int tile) {
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) acc[j][e] = out[j + 1][e];
             }
-        }
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-            cx[i] = nx[i];
-            cd[i] = nd[i];
         }
     }
     float *mine = a.partial + (long long)(blockIdx.x / ctiles) * a.C * (W + 1);
@@ -632,7 +623,8 @@ cudaError_t fwd_w(const ConvArgs &a, cudaStream_t st) {
     if ((long long)ct * a.total <= 148 * 32) {
         conv_few<T, VEC, W><<<ct * a.total, kThreads, 0, st>>>(a, ct);
     } else {
-        conv_fwd<T, VEC, W, 32><<<ct * ((a.total + 31) / 32), kThreads, 0, st>>>(a, ct);
+        constexpr int TT = kTile<T, VEC>;
+        conv_fwd<T, VEC, W><<<ct * ((a.total + TT - 1) / TT), kThreads, 0, st>>>(a, ct);
     }
     return cudaPeekAtLastError();
 }

@@ -109,6 +109,25 @@ __device__ __forceinline__ Raw<__nv_bfloat16, 8> pack(const float (&x)[8], Raw<_
     return Raw<__nv_bfloat16, 8>{make_uint4(w[0], w[1], w[2], w[3])};
 }
 
+// Copies one vector to shared memory without passing registers; the copying thread
+// may read it after copy_wait, which leaves its latest `pending` committed groups
+// under way.  (Vectors under 4 bytes are loaded and stored.)
+template <typename T, int VEC>
+__device__ __forceinline__ void copy_async(Raw<T, VEC> *to, const T *from) {
+    constexpr int bytes = sizeof(Raw<T, VEC>);
+    if constexpr (bytes >= 4) {
+        const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(bytes)
+                     : "memory");
+    } else {
+        *to = load_raw<T, VEC>(from);
+    }
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING> __device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
 // 1 / (1 + e^-x) by the approximate power of two and reciprocal: off by at most a few
 // float32 roundings (1e-6 relative for |x| up to 10); 0 where e^-x overflows.
 __device__ __forceinline__ float fast_sigmoid(float x) {
