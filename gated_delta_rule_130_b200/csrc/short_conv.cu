@@ -86,117 +86,136 @@ __device__ __forceinline__ void load_weights(const ConvArgs &a, int c, float (&w
     }
 }
 
-// Forward.  A block: kThreads * VEC channels and the tokens [t0, t0 + TT).  The block that
+// y = silu(z) in place of z
+template <int VEC> __device__ __forceinline__ void silu_vec(float (&z)[VEC]) {
+    float s[VEC];
+    fast_sigmoid<VEC>(z, s);
+    mul_vec<VEC>(z, s);
+}
+// d *= silu'(z) = sig (1 + z - z sig)
+template <int VEC>
+__device__ __forceinline__ void silu_grad_vec(const float (&z)[VEC], float (&d)[VEC]) {
+    float s[VEC], n[VEC], t[VEC];
+    fast_sigmoid<VEC>(z, s);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        n[e] = -s[e];
+        t[e] = z[e];
+    }
+    fma_vec<VEC>(n, z, t);  // z - z sig
+    mul_vec<VEC>(d, s);
+    fma_vec<VEC>(d, t, d);
+}
+
+// Forward.  A block: kThreads * VEC channels and the tokens [t0, t0 + tile).  The block that
 // holds a sequence's first token also takes the sequence's next W - 2 tokens, where
 // they lie behind its tile, and no other block does: so the held inputs of a slot are
 // read and written by one thread only.
 constexpr int kMine = 1, kPadding = 2, kFirst = 4, kHold = 8;
-struct __align__(16) Token {  // what a block knows of one of its tokens
-    int flags, start, end, slot;
-};
+constexpr int kMaxTile = 1024;  // tokens per block
 
-// All rows of the tile are on their way to shared memory at once, each thread's
-// own channels by itself, in groups of 8 rows.
-template <typename T, int VEC> constexpr int kTile = VEC * sizeof(T) > 8 ? 16 : 32;
+// The rows of x come through a ring of shared memory, each thread's own channels by
+// itself, S - 1 groups of B rows ahead.
+template <typename T, int VEC> constexpr int kFwdPerSM = VEC * sizeof(T) > 8 ? 5 : 6;
 
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kThreads)
-conv_fwd(ConvArgs a, unsigned ctiles) {
-    constexpr int TT = kTile<T, VEC>;
-    constexpr int NT = TT + W - 2;          // the tile and the tokens behind it
-    constexpr int B = 8;                    // rows per group
-    constexpr int NG = (NT + B - 1) / B;
-    static_assert(NT <= kThreads, "a thread per token");
-    static_assert(NG <= 5, "copy_wait's cases");
-    __shared__ __align__(16) Raw<T, VEC> rows[NT][kThreads];
-    __shared__ Token tok[NT];
-    __shared__ int seq[NT];
-    __shared__ __align__(8) unsigned char flag[(NT + 7) / 8 * 8];  // tok[].flags, packed
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+__global__ void __launch_bounds__(kThreads, kFwdPerSM<T, VEC>)
+conv_fwd(ConvArgs a, unsigned ctiles, int tile) {
+    constexpr int B = 8, S = VEC * sizeof(T) > 8 ? 2 : 4;
+    __shared__ __align__(16) Raw<T, VEC> ring[S][B][kThreads];
+    // of the tile's tokens and those behind it: the sequence (-1: none), the flags
+    __shared__ int seq[kMaxTile + W - 2];
+    __shared__ __align__(8) unsigned char flag[(kMaxTile + W - 2 + 7) / 8 * 8];
+    const int tid = threadIdx.x, lane = tid % 32;
     const int c = (int)((blockIdx.x % ctiles * kThreads + tid) * VEC);
-    const int t0 = (int)(blockIdx.x / ctiles * TT), t1 = min(t0 + TT, a.total);
-    const int far = min(t1 + W - 2, a.total) - 1;
+    const int t0 = (int)(blockIdx.x / ctiles) * tile, t1 = min(t0 + tile, a.total);
+    const int stop = min(t1 + W - 2, a.total);
     const bool live = c < a.C;
     const int cc = live ? c : 0;
     const T *x = static_cast<const T *>(a.x) + cc;
 
     // the rows are on their way while the sequences are found
+    const T *xa = x + (long long)t0 * a.x_stride;  // the row copied next
+    int copied = t0;
+    const auto copy_group = [&](int slot) {
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-#pragma unroll
-        for (int i = g * B; i < g * B + B && i < NT; ++i)
-            if (t0 + i <= far) copy_async<T, VEC>(&rows[i][tid], x + (t0 + i) * a.x_stride);
+        for (int i = 0; i < B; ++i) {
+            if (copied + i < stop) copy_async<T, VEC>(&ring[slot][i][tid], xa);
+            xa += a.x_stride;
+        }
+        copied += B;
         copy_commit();
-    }
+    };
+#pragma unroll
+    for (int g = 0; g < S - 1; ++g) copy_group(g);
     float win[W - 1][VEC];  // the inputs before the token
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
         const int s = t0 - (W - 1) + j;
         if (s >= 0) load_vec<T, VEC>(x + s * a.x_stride, win[j]);
     }
+    float w[W][VEC], b[VEC];
+    load_weights<T, VEC, W>(a, cc, w, b);
 
-    if (warp * 32 < NT) {
-        int lo = 0, hi = 0;
-        if (a.cu) {
-            lo = seq_of(a.cu, a.N, t0, lane);
-            hi = seq_of(a.cu, a.N, far, lane);
-        }
-        if (tid < NT) {
-            const int t = t0 + tid;
-            const Span sp = span_of(a, t <= far ? t : -1, lo, hi);
-            Token k{0, sp.start, sp.end, -1};
-            if (sp.start < sp.end) {
-                const int pos = t - sp.start;
-                const bool head = sp.start >= t0 && sp.start < t1;
-                if (pos < W - 1 ? head : t < t1) k.flags |= kMine;
-                if (pos == 0) k.flags |= kFirst;
-                if (a.states) {
-                    k.slot = a.slots ? a.slots[sp.n] : sp.n;
-                    if (k.slot < 0 || k.slot >= a.n_slots) k.flags |= kPadding;
-                    // with the last token that needs them the held inputs give way
-                    else if (t == min(sp.start + W - 2, sp.end - 1)) k.flags |= kHold;
-                }
+    int lo = 0, hi = 0;
+    if (a.cu) {
+        lo = seq_of(a.cu, a.N, t0, lane);
+        hi = seq_of(a.cu, a.N, stop - 1, lane);
+    }
+    const int padded = (stop - t0 + 31) / 32 * 32;
+    for (int i = tid; i < padded; i += kThreads) {
+        const int t = t0 + i;
+        const Span sp = span_of(a, t < stop ? t : -1, lo, hi);
+        const bool in = sp.start < sp.end;
+        int f = 0, slot = -1;
+        if (in) {
+            const int pos = t - sp.start;
+            const bool head = sp.start >= t0 && sp.start < t1;
+            if (pos < W - 1 ? head : t < t1) f |= kMine;
+            if (pos == 0) f |= kFirst;
+            if (a.states) {
+                slot = a.slots ? a.slots[sp.n] : sp.n;
+                if (slot < 0 || slot >= a.n_slots) f |= kPadding;
+                // with the last token that needs them the held inputs give way
+                else if (t == min(sp.start + W - 2, sp.end - 1)) f |= kHold;
             }
-            tok[tid] = k;
-            seq[tid] = sp.start < sp.end ? sp.n : -1;
+        }
+        if (a.states && a.slots) {
+            // of the sequences with tokens that name one slot the first has it: the warp
+            // looks at the sequences that its 32 tokens begin with or begin
+            const int n = in ? sp.n : -1, before = __shfl_up_sync(0xffffffffu, n, 1);
+            unsigned todo = __ballot_sync(0xffffffffu, in && !(f & kPadding) &&
+                                                           (lane == 0 || before != n));
+            while (todo) {
+                const int k = __ffs(todo) - 1;
+                todo &= todo - 1;
+                const int m = __shfl_sync(0xffffffffu, n, k);
+                const int want = __shfl_sync(0xffffffffu, slot, k);
+                int taken = 0;
+#pragma unroll 4
+                for (int l = lane; l < m; l += 32)
+                    if (a.slots[l] == want) taken |= !a.cu || a.cu[l] < a.cu[l + 1];
+                if (__any_sync(0xffffffffu, taken) && n == m) f |= kPadding;
+            }
+        }
+        if (t < stop) {
+            seq[i] = in ? sp.n : -1;
+            flag[i] = f;
         }
     }
-    __syncthreads();
-    if (a.states && a.slots) {
-        // of the sequences with tokens that name one slot the first has it
-        for (int i = warp; i < NT; i += kThreads / 32) {
-            const int n = seq[i];
-            if (n < 0 || (i > 0 && seq[i - 1] == n) || (tok[i].flags & kPadding)) continue;
-            const int want = tok[i].slot;
-            int taken = 0;
-            for (int k = lane; k < n; k += 32)
-                if (a.slots[k] == want) taken |= !a.cu || a.cu[k] < a.cu[k + 1];
-            if (__any_sync(0xffffffffu, taken))
-                for (int k = i + lane; k < NT; k += 32)
-                    if (seq[k] == n) tok[k].flags |= kPadding;
-        }
-        __syncthreads();
-    }
-    if (tid < (NT + 7) / 8 * 8) flag[tid] = tid < NT ? tok[tid].flags : 0;
+    if (tid < 8 && stop - t0 + tid < (int)sizeof(flag)) flag[stop - t0 + tid] = 0;
     __syncthreads();
     if (!live) return;
     int count = t1 - t0;
-#pragma unroll
-    for (int i = TT; i < NT; ++i)
-        if (t1 - t0 == TT && (tok[i].flags & kMine)) count = i + 1;
+    for (int i = t1 - t0; i < stop - t0; ++i)
+        if (flag[i] & kMine) count = i + 1;
 
     const int p = part_of(a, cc);
     T *y = static_cast<T *>(a.part[p]) + (cc - a.begin[p]) + t0 * a.part_stride[p];
-    float w[W][VEC], b[VEC];
-    load_weights<T, VEC, W>(a, cc, w, b);
-    for (int i0 = 0; i0 < count; i0 += B) {
-        switch (NG - 1 - i0 / B) {  // this group's rows have come
-            case 4: copy_wait<4>(); break;
-            case 3: copy_wait<3>(); break;
-            case 2: copy_wait<2>(); break;
-            case 1: copy_wait<1>(); break;
-            default: copy_wait<0>();
-        }
+    int slot = 0;
+    for (int i0 = 0; i0 < count; i0 += B, slot = slot + 1 == S ? 0 : slot + 1) {
+        copy_wait<S - 2>();  // this group's rows have come
+        copy_group(slot ? slot - 1 : S - 1);
         if (*reinterpret_cast<const unsigned long long *>(&flag[i0]) ==
             0x0101010101010101ull * kMine) {
             // eight tokens inside one sequence: no case to tell apart
@@ -207,16 +226,13 @@ conv_fwd(ConvArgs a, unsigned ctiles) {
                 for (int e = 0; e < VEC; ++e) in[j][e] = win[j][e];
 #pragma unroll
             for (int i = 0; i < B; ++i) {
-                widen(rows[i0 + i][tid], in[W - 1 + i]);
+                widen(ring[slot][i][tid], in[W - 1 + i]);
                 float z[VEC];
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) z[e] = b[e];
 #pragma unroll
                 for (int j = 0; j < W; ++j) fma_vec<VEC>(w[j], in[i + j], z);
-                if (a.silu) {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) z[e] *= fast_sigmoid(z[e]);
-                }
+                if (a.silu) silu_vec<VEC>(z);
                 store_vec(y, z);
                 y += a.part_stride[p];
             }
@@ -227,66 +243,62 @@ conv_fwd(ConvArgs a, unsigned ctiles) {
             continue;
         }
 #pragma unroll 1
-        for (int i = 0; i < B; ++i) {
-            if (i0 + i < count) {
-                const int f = tok[i0 + i].flags;
-                T *held = nullptr;
-                if (f & (kFirst | kHold)) {
-                    if (a.states && !(f & kPadding))
-                        held = static_cast<T *>(a.states) +
-                               (long long)tok[i0 + i].slot * (W - 1) * a.C + cc;
-                    if (f & kFirst) {
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j) {
-                            if (held) {
-                                load_vec<T, VEC>(held + (long long)j * a.C, win[j]);
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < VEC; ++e) win[j][e] = 0.f;
-                            }
-                        }
-                    }
-                }
-                float now[VEC], z[VEC];
-                widen(rows[i0 + i][tid], now);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) z[e] = b[e];
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) fma_vec<VEC>(w[j], win[j], z);
-                fma_vec<VEC>(w[W - 1], now, z);
-                if (f & kMine) {
-                    if (a.silu) {
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) z[e] *= fast_sigmoid(z[e]);
-                    }
-                    if (f & kPadding) {
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) z[e] = 0.f;
-                    }
-                    store_vec(y, z);
-                }
-                y += a.part_stride[p];
-#pragma unroll
-                for (int j = 0; j + 1 < W - 1; ++j)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) win[W - 2][e] = now[e];
-                if (held && (f & kMine) && (f & kHold)) {
-                    // the sequence's last inputs; win has them where it is that short
-                    const int end = tok[i0 + i].end;
-                    const bool is_short = end - tok[i0 + i].start < W - 1;
+        for (int i = 0; i < B && i0 + i < count; ++i) {
+            const int f = flag[i0 + i];
+            T *held = nullptr;
+            int start = 0, end = 0;
+            if (f & (kFirst | kHold)) {
+                const int n = seq[i0 + i];
+                start = a.cu ? a.cu[n] : n;
+                end = a.cu ? a.cu[n + 1] : n + 1;
+                if (a.states && !(f & kPadding))
+                    held = static_cast<T *>(a.states) +
+                           (long long)(a.slots ? a.slots[n] : n) * (W - 1) * a.C + cc;
+                if (f & kFirst) {
 #pragma unroll
                     for (int j = 0; j < W - 1; ++j) {
-                        float v[VEC];
-                        if (is_short) {
-#pragma unroll
-                            for (int e = 0; e < VEC; ++e) v[e] = win[j][e];
+                        if (held) {
+                            load_vec<T, VEC>(held + (long long)j * a.C, win[j]);
                         } else {
-                            load_vec<T, VEC>(x + (end - (W - 1) + j) * a.x_stride, v);
+#pragma unroll
+                            for (int e = 0; e < VEC; ++e) win[j][e] = 0.f;
                         }
-                        store_vec(held + (long long)j * a.C, v);
                     }
+                }
+            }
+            float now[VEC], z[VEC];
+            widen(ring[slot][i][tid], now);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) z[e] = b[e];
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) fma_vec<VEC>(w[j], win[j], z);
+            fma_vec<VEC>(w[W - 1], now, z);
+            if (f & kMine) {
+                if (a.silu) silu_vec<VEC>(z);
+                if (f & kPadding) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) z[e] = 0.f;
+                }
+                store_vec(y, z);
+            }
+            y += a.part_stride[p];
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) win[j][e] = j + 1 < W - 1 ? win[j + 1][e] : now[e];
+            if (held && (f & kMine) && (f & kHold)) {
+                // the sequence's last inputs; win has them where it is that short
+                const bool is_short = end - start < W - 1;
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) {
+                    float v[VEC];
+                    if (is_short) {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) v[e] = win[j][e];
+                    } else {
+                        load_vec<T, VEC>(x + (end - (W - 1) + j) * a.x_stride, v);
+                    }
+                    store_vec(held + (long long)j * a.C, v);
                 }
             }
         }
@@ -363,11 +375,10 @@ conv_few(ConvArgs a, unsigned ctiles) {
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) fma_vec<VEC>(w[j], win[j], z);
         fma_vec<VEC>(w[W - 1], now, z);
+        if (a.silu) silu_vec<VEC>(z);
+        if (zero)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            if (a.silu) z[e] *= fast_sigmoid(z[e]);
-            if (zero) z[e] = 0.f;
-        }
+            for (int e = 0; e < VEC; ++e) z[e] = 0.f;
         store_vec(y, z);
         y += a.part_stride[p];
 #pragma unroll
@@ -386,8 +397,7 @@ conv_few(ConvArgs a, unsigned ctiles) {
     }
 }
 
-constexpr int kMaxTile = 1024;  // tokens per block of the backward
-// Its blocks per SM: 5 of 102 registers a thread.
+// Blocks of the backward per SM: 5 of 102 registers a thread.
 template <typename T, int VEC> constexpr int kBwdPerSM = VEC * sizeof(T) > 8 ? 4 : 5;
 
 // Backward.  A block: kThreads * VEC channels and the tokens [t0, t0 + tile): their dx
@@ -493,19 +503,14 @@ conv_bwd(ConvArgs a, unsigned ctiles, int tile) {
                     for (int e = 0; e < VEC; ++e) z[e] = b[e];
 #pragma unroll
                     for (int j = 0; j < W; ++j) fma_vec<VEC>(w[j], in[i + j], z);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float sig = fast_sigmoid(z[e]);
-                        d[e] *= fmaf(sig, fmaf(-z[e], sig, z[e]), sig);
-                    }
+                    silu_grad_vec<VEC>(z, d);
                 }
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
                     fma_vec<VEC>(w[j], d, out[i + j]);
                     fma_vec<VEC>(d, in[i + j], dw[j]);
                 }
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) db[e] += d[e];
+                add_vec<VEC>(db, d);
                 store_vec(dx, out[i]);
                 dx += a.C;
             }
@@ -541,11 +546,7 @@ conv_bwd(ConvArgs a, unsigned ctiles, int tile) {
                         for (int e = 0; e < VEC; ++e) z[e] = b[e];
 #pragma unroll
                         for (int j = 0; j < W; ++j) fma_vec<VEC>(w[j], in[j], z);
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            const float sig = fast_sigmoid(z[e]);
-                            d[e] *= fmaf(sig, fmaf(-z[e], sig, z[e]), sig);
-                        }
+                        silu_grad_vec<VEC>(z, d);
                     }
 #pragma unroll
                     for (int j = 0; j < W; ++j)
@@ -617,26 +618,28 @@ bool vectors_fit(const ConvArgs &a) {
 
 unsigned channel_tiles(int C, int vec) { return (C + kThreads * vec - 1) / (kThreads * vec); }
 
+// Tokens per block such that `per_sm` blocks per SM take them all at once, at least 8.
+int tile_of(int total, unsigned ctiles, int per_sm) {
+    const int rows = 148 * per_sm / (int)ctiles > 1 ? 148 * per_sm / (int)ctiles : 1;
+    const int tile = ((total + rows - 1) / rows + 7) / 8 * 8;
+    return tile > kMaxTile ? kMaxTile : tile;
+}
+
 template <typename T, int VEC, int W>
 cudaError_t fwd_w(const ConvArgs &a, cudaStream_t st) {
     const unsigned ct = channel_tiles(a.C, VEC);
     if ((long long)ct * a.total <= 148 * 32) {
         conv_few<T, VEC, W><<<ct * a.total, kThreads, 0, st>>>(a, ct);
     } else {
-        constexpr int TT = kTile<T, VEC>;
-        conv_fwd<T, VEC, W><<<ct * ((a.total + TT - 1) / TT), kThreads, 0, st>>>(a, ct);
+        const int tile = tile_of(a.total, ct, kFwdPerSM<T, VEC>);
+        conv_fwd<T, VEC, W><<<ct * ((a.total + tile - 1) / tile), kThreads, 0, st>>>(a, ct, tile);
     }
     return cudaPeekAtLastError();
 }
 
-// Tokens per block of the backward: blocks of 5 channels-of-128-threads per SM fill the
-// GPU once.  Sized for vectors of 4 channels whatever the call's alignment is, so that
-// the workspace depends on the sizes alone.
-int bwd_tile(int total, int C) {
-    const int ct = (int)channel_tiles(C, 4), rows = 148 * 5 / ct > 1 ? 148 * 5 / ct : 1;
-    const int tile = (total + rows - 1) / rows;
-    return tile < 16 ? 16 : tile > kMaxTile ? kMaxTile : tile;
-}
+// The backward's tile.  Sized for vectors of 4 channels and 5 blocks per SM whatever
+// the call's alignment and type are, so that the workspace depends on the sizes alone.
+int bwd_tile(int total, int C) { return tile_of(total, channel_tiles(C, 4), 5); }
 
 template <typename T, int VEC, int W>
 cudaError_t bwd_w(const ConvArgs &a, cudaStream_t st) {

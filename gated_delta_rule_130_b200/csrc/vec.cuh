@@ -95,6 +95,37 @@ __device__ __forceinline__ void fma_vec(const float (&x)[VEC], const float (&y)[
     }
 }
 
+// x *= y
+template <int VEC>
+__device__ __forceinline__ void mul_vec(float (&x)[VEC], const float (&y)[VEC]) {
+    if constexpr (VEC % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+            const float2 z = __fmul2_rn(make_float2(x[e], x[e + 1]), make_float2(y[e], y[e + 1]));
+            x[e] = z.x;
+            x[e + 1] = z.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[e] *= y[e];
+    }
+}
+// x += y
+template <int VEC>
+__device__ __forceinline__ void add_vec(float (&x)[VEC], const float (&y)[VEC]) {
+    if constexpr (VEC % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+            const float2 z = __fadd2_rn(make_float2(x[e], x[e + 1]), make_float2(y[e], y[e + 1]));
+            x[e] = z.x;
+            x[e + 1] = z.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[e] += y[e];
+    }
+}
+
 // x packed to T, as one load would have brought it.
 __device__ __forceinline__ Raw<float, 4> pack(const float (&x)[4], Raw<float, 4>) {
     return Raw<float, 4>{make_float4(x[0], x[1], x[2], x[3])};
@@ -135,6 +166,26 @@ __device__ __forceinline__ float fast_sigmoid(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
     return r;
+}
+// The same of VEC elements, two per instruction where the unit allows.
+template <int VEC>
+__device__ __forceinline__ void fast_sigmoid(const float (&x)[VEC], float (&s)[VEC]) {
+    if constexpr (VEC % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+            const float2 m = __fmul2_rn(make_float2(x[i], x[i + 1]),
+                                        make_float2(-1.4426950408889634f, -1.4426950408889634f));
+            float2 e;
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(m.x));
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(m.y));
+            e = __fadd2_rn(e, make_float2(1.f, 1.f));
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s[i]) : "f"(e.x));
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s[i + 1]) : "f"(e.y));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s[i] = fast_sigmoid(x[i]);
+    }
 }
 
 }  // namespace gdn
