@@ -112,16 +112,18 @@ __device__ __forceinline__ void silu_grad_vec(const float (&z)[VEC], float (&d)[
 // they lie behind its tile, and no other block does: so the held inputs of a slot are
 // read and written by one thread only.
 constexpr int kMine = 1, kPadding = 2, kFirst = 4, kHold = 8;
-constexpr int kMaxTile = 1024;  // tokens per block
+constexpr int kMaxTile = 512;  // tokens per block
 
 // The rows of x come through a ring of shared memory, each thread's own channels by
 // itself, S - 1 groups of B rows ahead.
-template <typename T, int VEC> constexpr int kFwdPerSM = VEC * sizeof(T) > 8 ? 5 : 6;
+// Three groups in the ring and 7 blocks per SM took 73.2 us on 16384 x 6144, 6 blocks
+// 74.6; four groups and 6 or 5 blocks, of which 4 ran at once, 85.7 and 88.6.
+template <typename T, int VEC> constexpr int kFwdPerSM = VEC * sizeof(T) > 8 ? 5 : 7;
 
 template <typename T, int VEC, int W>
 __global__ void __launch_bounds__(kThreads, kFwdPerSM<T, VEC>)
 conv_fwd(ConvArgs a, unsigned ctiles, int tile) {
-    constexpr int B = 8, S = VEC * sizeof(T) > 8 ? 2 : 4;
+    constexpr int B = 8, S = VEC * sizeof(T) > 8 ? 2 : 3;
     __shared__ __align__(16) Raw<T, VEC> ring[S][B][kThreads];
     // of the tile's tokens and those behind it: the sequence (-1: none), the flags
     __shared__ int seq[kMaxTile + W - 2];
@@ -397,15 +399,16 @@ conv_few(ConvArgs a, unsigned ctiles) {
     }
 }
 
-// Blocks of the backward per SM: 5 of 102 registers a thread.
-template <typename T, int VEC> constexpr int kBwdPerSM = VEC * sizeof(T) > 8 ? 4 : 5;
+// Blocks of the backward per SM: 4 of 120 registers a thread (5 of 96 spill, and took
+// 163.5 us on 16384 x 6144 where these take 119.0 us).
+constexpr int kBwdPerSM = 4;
 
 // Backward.  A block: kThreads * VEC channels and the tokens [t0, t0 + tile): their dx
 // (dz of the W - 1 tokens behind the tile is formed again) and their share of dw.
 // The rows of x and dy come through a ring of shared memory, each thread's own
 // channels by itself, S - 1 groups of B rows ahead.
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kThreads, kBwdPerSM<T, VEC>)
+__global__ void __launch_bounds__(kThreads, kBwdPerSM)
 conv_bwd(ConvArgs a, unsigned ctiles, int tile) {
     constexpr int B = 4, S = VEC * sizeof(T) > 8 ? 2 : 4;
     __shared__ __align__(16) Raw<T, VEC> ring[2][S][B][kThreads];
@@ -637,9 +640,9 @@ cudaError_t fwd_w(const ConvArgs &a, cudaStream_t st) {
     return cudaPeekAtLastError();
 }
 
-// The backward's tile.  Sized for vectors of 4 channels and 5 blocks per SM whatever
+// The backward's tile.  Sized for vectors of 4 channels whatever
 // the call's alignment and type are, so that the workspace depends on the sizes alone.
-int bwd_tile(int total, int C) { return tile_of(total, channel_tiles(C, 4), 5); }
+int bwd_tile(int total, int C) { return tile_of(total, channel_tiles(C, 4), kBwdPerSM); }
 
 template <typename T, int VEC, int W>
 cudaError_t bwd_w(const ConvArgs &a, cudaStream_t st) {
