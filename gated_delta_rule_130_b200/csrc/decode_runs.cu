@@ -29,6 +29,7 @@ namespace {
 
 constexpr int kTok = 8;       // tokens taken at once
 constexpr int kMaxWarps = 8;  // per block
+constexpr int kTokenBlocks = 4, kChunkBlocks = 3;  // blocks per SM
 
 // Sums of NV values per lane over LW neighbouring lanes: while lanes and values
 // last, each step hands half of the values to the partner lane; afterwards lane l
@@ -57,9 +58,14 @@ __device__ __forceinline__ int reduce_scatter(float (&x)[NV], int lane) {
     return first;
 }
 
-template <bool VEC>
+// How a row of Dk key channels is read: element by element, by float4, or by float4
+// with Dk known to fill the lanes (no element of a row needs a test).
+enum Rows { kAny, kVec, kFull };
+
+template <int K>
 __device__ __forceinline__ float4 load_state(const float *row, int c, int Dk) {
-    if (VEC) return c < Dk ? *reinterpret_cast<const float4 *>(row + c) : make_float4(0, 0, 0, 0);
+    if (K == kFull) return *reinterpret_cast<const float4 *>(row + c);
+    if (K == kVec) return c < Dk ? *reinterpret_cast<const float4 *>(row + c) : make_float4(0, 0, 0, 0);
     float4 s;
     s.x = c < Dk ? row[c] : 0.f;
     s.y = c + 1 < Dk ? row[c + 1] : 0.f;
@@ -67,10 +73,10 @@ __device__ __forceinline__ float4 load_state(const float *row, int c, int Dk) {
     s.w = c + 3 < Dk ? row[c + 3] : 0.f;
     return s;
 }
-template <bool VEC>
+template <int K>
 __device__ __forceinline__ void store_state(float *row, int c, int Dk, float4 s) {
-    if (VEC) {
-        if (c < Dk) *reinterpret_cast<float4 *>(row + c) = s;
+    if (K != kAny) {
+        if (K == kFull || c < Dk) *reinterpret_cast<float4 *>(row + c) = s;
         return;
     }
     if (c < Dk) row[c] = s.x;
@@ -86,9 +92,10 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 
 // Elements c .. c + 3 of a row of k or q, widened; 0 from Dk on.
-template <bool VEC, typename T>
+template <int K, typename T>
 __device__ __forceinline__ float4 load_key(const T *row, int c, int Dk, bool aligned) {
-    if (VEC && aligned) return c < Dk ? load4(row + c) : make_float4(0, 0, 0, 0);
+    if (K != kAny && aligned)
+        return K == kFull || c < Dk ? load4(row + c) : make_float4(0, 0, 0, 0);
     return make_float4(c < Dk ? to_f32(row[c]) : 0.f, c + 1 < Dk ? to_f32(row[c + 1]) : 0.f,
                        c + 2 < Dk ? to_f32(row[c + 2]) : 0.f, c + 3 < Dk ? to_f32(row[c + 3]) : 0.f);
 }
@@ -96,32 +103,24 @@ __device__ __forceinline__ float4 load_key(const T *row, int c, int Dk, bool ali
 __device__ __forceinline__ float2 lo2(const float4 &x) { return make_float2(x.x, x.y); }
 __device__ __forceinline__ float2 hi2(const float4 &x) { return make_float2(x.z, x.w); }
 
-// LW lanes share a row, V float4 each; R rows per lane group, so ROWS rows per warp.
-constexpr int R = 4;
-template <int LW> constexpr int kRows = R * (32 / LW);
+// LW lanes share a row, V float4 each; R rows per lane group, so this many per warp.
+template <int LW, int R> constexpr int kRows = R * (32 / LW);
 
-// acc[r] += s_r . k, acc[R + r] += s_r . q over this lane's elements.
-template <int V>
-__device__ __forceinline__ void row_dots(const float4 (&s)[R][V], const float4 (&k4)[V],
-                                         const float4 (&q4)[V], float (&x)[2 * R]) {
-    float2 x2[2 * R];
+// acc[r] += s_r . k, acc[R + r] += s_r . q over the elements of one float4 per row.
+template <int R, int V>
+__device__ __forceinline__ void row_dots(const float4 (&s)[R][V], int v, const float4 &k4,
+                                         const float4 &q4, float2 (&acc)[2 * R]) {
 #pragma unroll
-    for (int i = 0; i < 2 * R; ++i) x2[i] = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            x2[r] = __ffma2_rn(lo2(s[r][v]), lo2(k4[v]), x2[r]);
-            x2[r] = __ffma2_rn(hi2(s[r][v]), hi2(k4[v]), x2[r]);
-            x2[R + r] = __ffma2_rn(lo2(s[r][v]), lo2(q4[v]), x2[R + r]);
-            x2[R + r] = __ffma2_rn(hi2(s[r][v]), hi2(q4[v]), x2[R + r]);
-        }
-#pragma unroll
-    for (int i = 0; i < 2 * R; ++i) x[i] = x2[i].x + x2[i].y;
+    for (int r = 0; r < R; ++r) {
+        acc[r] = __ffma2_rn(lo2(s[r][v]), lo2(k4), acc[r]);
+        acc[r] = __ffma2_rn(hi2(s[r][v]), hi2(k4), acc[r]);
+        acc[R + r] = __ffma2_rn(lo2(s[r][v]), lo2(q4), acc[R + r]);
+        acc[R + r] = __ffma2_rn(hi2(s[r][v]), hi2(q4), acc[R + r]);
+    }
 }
 
 // s_r <- g s_r
-template <int V>
+template <int R, int V>
 __device__ __forceinline__ void scale_rows(float4 (&s)[R][V], float g) {
     const float2 g2 = make_float2(g, g);
 #pragma unroll
@@ -132,47 +131,60 @@ __device__ __forceinline__ void scale_rows(float4 (&s)[R][V], float g) {
             s[r][v] = make_float4(lo.x, lo.y, hi.x, hi.y);
         }
 }
-// s_r <- s_r + u_r k
-template <int V>
-__device__ __forceinline__ void add_rows(float4 (&s)[R][V], const float (&u)[R],
-                                         const float4 (&k4)[V]) {
+// s_r <- s_r + u_r k, one float4 per row.
+template <int R, int V>
+__device__ __forceinline__ void add_rows(float4 (&s)[R][V], int v, const float (&u)[R],
+                                         const float4 &k4) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const float2 uu = make_float2(u[r], u[r]);
-            const float2 lo = __ffma2_rn(uu, lo2(k4[v]), lo2(s[r][v]));
-            const float2 hi = __ffma2_rn(uu, hi2(k4[v]), hi2(s[r][v]));
-            s[r][v] = make_float4(lo.x, lo.y, hi.x, hi.y);
-        }
+    for (int r = 0; r < R; ++r) {
+        const float2 uu = make_float2(u[r], u[r]);
+        const float2 lo = __ffma2_rn(uu, lo2(k4), lo2(s[r][v]));
+        const float2 hi = __ffma2_rn(uu, hi2(k4), hi2(s[r][v]));
+        s[r][v] = make_float4(lo.x, lo.y, hi.x, hi.y);
+    }
+}
+
+// The decay and the write strength of a token as the recurrence uses them; with logits
+// alpha = exp(-softplus(x)) = 1 / (1 + e^x).
+__device__ __forceinline__ float2 decay_pair(float la, float be, unsigned flags) {
+    if (flags & kFlagGateLogits) return make_float2(sigmoid(-la), sigmoid(be));
+    return make_float2(expf(la), be);
 }
 
 // A warp's rows of the state from wrow on, zero from Dv on.
-template <int LW, int V, bool VEC>
+template <int LW, int R, int V, int K>
 __device__ __forceinline__ void load_rows(const RunsArgs &a, const float *state, int wrow, int lane,
                                           bool run, float4 (&s)[R][V]) {
+    const int Dk = K == kFull ? LW * V * 4 : a.Dk;
+    const float *p = state + (long long)(wrow + lane / LW * R) * Dk;
+    const bool all = run && wrow + kRows<LW, R> <= a.Dv;
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int row = wrow + lane / LW * R + r;
-            s[r][v] = run && row < a.Dv ? load_state<VEC>(state + (long long)row * a.Dk,
-                                                          4 * (v * LW + lane % LW), a.Dk)
-                                        : make_float4(0, 0, 0, 0);
-        }
+        for (int v = 0; v < V; ++v)
+            s[r][v] = all || (run && wrow + lane / LW * R + r < a.Dv)
+                          ? load_state<K>(p + r * Dk, 4 * (v * LW + lane % LW), Dk)
+                          : make_float4(0, 0, 0, 0);
 }
-template <int LW, int V, bool VEC>
+template <int LW, int R, int V, int K>
 __device__ __forceinline__ void store_rows(const RunsArgs &a, float *state, int wrow, int lane,
                                            const float4 (&s)[R][V]) {
+    const int Dk = K == kFull ? LW * V * 4 : a.Dk;
+    float *p = state + (long long)(wrow + lane / LW * R) * Dk;
+    if (wrow + kRows<LW, R> <= a.Dv) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                store_state<K>(p + r * Dk, 4 * (v * LW + lane % LW), Dk, s[r][v]);
+        return;
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int row = wrow + lane / LW * R + r;
-            if (row < a.Dv)
-                store_state<VEC>(state + (long long)row * a.Dk, 4 * (v * LW + lane % LW), a.Dk,
-                                 s[r][v]);
-        }
+        for (int v = 0; v < V; ++v)
+            if (wrow + lane / LW * R + r < a.Dv)
+                store_state<K>(p + r * Dk, 4 * (v * LW + lane % LW), Dk, s[r][v]);
 }
 
 // Whether an earlier sequence with tokens names this slot (seen by every lane that
@@ -184,103 +196,129 @@ __device__ __forceinline__ int slot_taken(const RunsArgs &a, int n, int slot, in
     return taken;
 }
 
-// Runs of one token: every warp for itself, k, q and their norms in registers and no
-// barrier, so the pass is as good as its loads and stores of the state.
-template <typename T, int LW, int V, bool VEC>
-__device__ __forceinline__ void one_token(const RunsArgs &a, float *state, int n, int h, int t,
-                                          int slot, bool run, int row0, int tiles) {
-    constexpr int ROWS = kRows<LW>, NK = 2 * R > LW ? 2 * R / LW : 1;
+// Token by token: every warp for itself, k, q and their norms in registers and no
+// barrier, so that a run of one token costs little beyond the loads and stores of
+// the state.  A block: `tiles` times warps * ROWS value channels of one value head of
+// one sequence.
+template <typename T, int LW, int R, int V, int K>
+__global__ void __launch_bounds__(32 * kMaxWarps, kTokenBlocks)
+decode_tokens_kernel(RunsArgs a, int row_blocks, int tiles) {
+    constexpr int ROWS = kRows<LW, R>, NK = 2 * R > LW ? 2 * R / LW : 1;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
     const int sub = lane % LW;
+    const int nh = blockIdx.x / row_blocks;
+    const int n = nh / a.Hv, h = nh % a.Hv;
+    const int t0 = a.cu ? a.cu[n] : n, t1 = a.cu ? a.cu[n + 1] : n + 1;
+    const int slot = a.slots ? a.slots[n] : n;
+    if (t0 < 0 || t1 > a.total || t0 >= t1) return;  // empty, or offsets that are none
+    bool run = slot >= 0 && slot < a.n_slots;
+    const int row0 = blockIdx.x % row_blocks * tiles * warps * ROWS;
+    float *state = a.states + ((long long)(run ? slot : 0) * a.Hv + h) * a.Dv * a.Dk;
     const int hk = h / (a.Hv / a.Hk);
-    const T *kr = static_cast<const T *>(a.k) + t * a.k_stride + (long long)hk * a.Dk;
-    const T *qr = a.q ? static_cast<const T *>(a.q) + t * a.q_stride + (long long)hk * a.Dk : nullptr;
-    const T *vr = static_cast<const T *>(a.v) + t * a.v_stride + (long long)h * a.Dv;
-    T *op = a.o ? static_cast<T *>(a.o) + ((long long)t * a.Hv + h) * a.Dv : nullptr;
-    const bool rows_aligned = a.k_stride % 4 == 0 && a.q_stride % 4 == 0;
-
-    float4 s[R][V], k4[V], q4[V];
-    load_rows<LW, V, VEC>(a, state, row0 + warp * ROWS, lane, run, s);
-    float g0 = 0.f, g1 = 0.f;
-    if (run) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            k4[v] = load_key<VEC>(kr, 4 * (v * LW + sub), a.Dk, rows_aligned);
-            q4[v] = qr ? load_key<VEC>(qr, 4 * (v * LW + sub), a.Dk, rows_aligned)
-                       : make_float4(0, 0, 0, 0);
-        }
-        g0 = a.log_alpha[t * a.la_stride + h];
-        g1 = a.beta[t * a.be_stride + h];
-        if (a.update && a.slots &&
-            __any_sync(0xffffffffu, slot_taken(a, n, slot, lane, 32)))
-            run = false;
-    }
-    if (!run) {  // a row of padding: its outputs are zero, nothing else is touched
-        if (op)
-            for (int i = threadIdx.x; i < tiles * warps * ROWS && row0 + i < a.Dv; i += blockDim.x)
-                op[row0 + i] = from_f32<T>(0.f);
-        return;
-    }
-    float kk = 0.f, qq = 0.f, kq = 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        kk += k4[v].x * k4[v].x + k4[v].y * k4[v].y + k4[v].z * k4[v].z + k4[v].w * k4[v].w;
-        qq += q4[v].x * q4[v].x + q4[v].y * q4[v].y + q4[v].z * q4[v].z + q4[v].w * q4[v].w;
-        kq += k4[v].x * q4[v].x + k4[v].y * q4[v].y + k4[v].z * q4[v].z + k4[v].w * q4[v].w;
-    }
-#pragma unroll
-    for (int off = LW / 2; off > 0; off >>= 1) {
-        kk += __shfl_xor_sync(0xffffffffu, kk, off);
-        qq += __shfl_xor_sync(0xffffffffu, qq, off);
-        kq += __shfl_xor_sync(0xffffffffu, kq, off);
-    }
+    const T *kr = static_cast<const T *>(a.k) + (long long)hk * a.Dk;
+    const T *qr = a.q ? static_cast<const T *>(a.q) + (long long)hk * a.Dk : nullptr;
+    const T *vr = static_cast<const T *>(a.v) + (long long)h * a.Dv;
+    T *op = a.o ? static_cast<T *>(a.o) + (long long)h * a.Dv : nullptr;
+    const bool aligned = a.k_stride % 4 == 0 && a.q_stride % 4 == 0;
     const bool unit = a.flags & kFlagL2Norm;
-    const float rk = unit ? rsqrtf(kk + kNormEps) : 1.f, rq = unit ? rsqrtf(qq + kNormEps) : 1.f;
-    const float2 gp = gate_pair(g0, g1, a.flags);
-    const float alpha = expf(gp.x), beta = gp.y;
+
+    // a lane ends up with NK of a row group's sums: its rows' S.k in the lower half of
+    // the lanes, their S.q in the upper half
+    const int first = LW >= 2 * R ? sub / (LW / (2 * R)) : sub * NK;
+    float4 k4[V], q4[V];
+    float kq = 0.f, rk = 1.f, rq = 1.f, alpha = 0.f, beta = 0.f;
     for (int tile = 0; tile < tiles; ++tile) {
         const int wrow = row0 + (tile * warps + warp) * ROWS;
         if (wrow >= a.Dv) return;
-        if (tile) load_rows<LW, V, VEC>(a, state, wrow, lane, true, s);
-        // a lane ends up with NK of the sums: rows' a in the lower half of its group,
-        // their b in the upper half; the lower half forms u and hands it over
+        float4 s[R][V];
+        load_rows<LW, R, V, K>(a, state, wrow, lane, run, s);
         const int grow = wrow + lane / LW * R;  // the lane group's first row
-        const int first = LW >= 2 * R ? sub / (LW / (2 * R)) : sub * NK;
-        float vv[NK];
+        for (int t = t0; t < t1; ++t) {
+            float vv[NK];
 #pragma unroll
-        for (int i = 0; i < NK; ++i) {
-            const int row = grow + (first + i) % R;
-            vv[i] = row < a.Dv ? to_f32(vr[row]) : 0.f;
-        }
-        float x[2 * R];
-        row_dots<V>(s, k4, q4, x);
-        reduce_scatter<2 * R, LW>(x, lane);
-        float un[NK];
+            for (int i = 0; i < NK; ++i) {
+                const int row = grow + (first + i) % R;
+                vv[i] = run && row < a.Dv ? to_f32(vr[t * a.v_stride + row]) : 0.f;
+            }
+            if (run && (tile == 0 || t1 - t0 > 1)) {  // tiles share the token of a run of one
 #pragma unroll
-        for (int i = 0; i < NK; ++i) {
-            const float mine = beta * (vv[i] - alpha * rk * x[i]);  // meant in the lower half
-            un[i] = __shfl_sync(0xffffffffu, mine, lane % (LW / 2), LW);
-            const int row = grow + (first + i) % R;
-            if (op && first + i >= R && row < a.Dv)
-                op[row] = from_f32<T>(rq * (alpha * x[i] + un[i] * rk * kq));
-        }
-        if (!a.update) continue;
-        float u[R];
+                for (int v = 0; v < V; ++v) {
+                    k4[v] = load_key<K>(kr + t * a.k_stride, 4 * (v * LW + sub), a.Dk, aligned);
+                    q4[v] = qr ? load_key<K>(qr + t * a.q_stride, 4 * (v * LW + sub), a.Dk, aligned)
+                               : make_float4(0, 0, 0, 0);
+                }
+                const float g0 = a.log_alpha[t * a.la_stride + h], g1 = a.beta[t * a.be_stride + h];
+                if (t == t0 && tile == 0 && a.update && a.slots &&
+                    __any_sync(0xffffffffu, slot_taken(a, n, slot, lane, 32)))
+                    run = false;
+                float kk = 0.f, qq = 0.f;
+                kq = 0.f;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-            u[r] = rk * __shfl_sync(0xffffffffu, un[r % NK], r / NK * (LW >= 2 * R ? LW / (2 * R) : 1),
+                for (int v = 0; v < V; ++v) {
+                    kk += k4[v].x * k4[v].x + k4[v].y * k4[v].y + k4[v].z * k4[v].z + k4[v].w * k4[v].w;
+                    qq += q4[v].x * q4[v].x + q4[v].y * q4[v].y + q4[v].z * q4[v].z + q4[v].w * q4[v].w;
+                    kq += k4[v].x * q4[v].x + k4[v].y * q4[v].y + k4[v].z * q4[v].z + k4[v].w * q4[v].w;
+                }
+#pragma unroll
+                for (int off = LW / 2; off > 0; off >>= 1) {
+                    kq += __shfl_xor_sync(0xffffffffu, kq, off);
+                    if (unit) {
+                        kk += __shfl_xor_sync(0xffffffffu, kk, off);
+                        qq += __shfl_xor_sync(0xffffffffu, qq, off);
+                    }
+                }
+                if (unit) {
+                    rk = rsqrtf(kk + kNormEps);
+                    rq = rsqrtf(qq + kNormEps);
+                }
+                const float2 gp = decay_pair(g0, g1, a.flags);
+                alpha = gp.x;
+                beta = gp.y;
+            }
+            if (!run) {  // a row of padding: its outputs are zero, nothing else is touched
+                if (op)
+                    for (int i = lane; i < ROWS && wrow + i < a.Dv; i += 32)
+                        op[(long long)t * a.Hv * a.Dv + wrow + i] = from_f32<T>(0.f);
+                continue;
+            }
+            float2 acc[2 * R];
+            float x[2 * R], un[NK];
+#pragma unroll
+            for (int i = 0; i < 2 * R; ++i) acc[i] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int v = 0; v < V; ++v) row_dots<R, V>(s, v, k4[v], q4[v], acc);
+#pragma unroll
+            for (int i = 0; i < 2 * R; ++i) x[i] = acc[i].x + acc[i].y;
+            reduce_scatter<2 * R, LW>(x, lane);
+#pragma unroll
+            for (int i = 0; i < NK; ++i) {
+                // u = beta (v - alpha S.k), in the lanes that hold S.k, for the others too
+                un[i] = __shfl_sync(0xffffffffu, beta * (vv[i] - alpha * rk * x[i]), sub % (LW / 2),
                                     LW);
-        scale_rows<V>(s, alpha);
-        add_rows<V>(s, u, k4);
-        store_rows<LW, V, VEC>(a, state, wrow, lane, s);
+                const int row = grow + (first + i) % R;
+                if (op && first + i >= R && row < a.Dv)
+                    op[(long long)t * a.Hv * a.Dv + row] =
+                        from_f32<T>(rq * (alpha * x[i] + un[i] * rk * kq));
+            }
+            if (!a.update && t + 1 == t1) break;
+            float u[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                u[r] = rk * __shfl_sync(0xffffffffu, un[r % NK],
+                                        r / NK * (LW >= 2 * R ? LW / (2 * R) : 1), LW);
+            scale_rows<R, V>(s, alpha);
+#pragma unroll
+            for (int v = 0; v < V; ++v) add_rows<R, V>(s, v, u, k4[v]);
+        }
+        if (run && a.update) store_rows<LW, R, V, K>(a, state, wrow, lane, s);
     }
 }
 
-// A block: `tiles` times warps * ROWS value channels of one value head of one sequence.
-template <typename T, int LW, int V, bool VEC>
-__global__ void __launch_bounds__(32 * kMaxWarps, 3)
-decode_runs_kernel(RunsArgs a, int row_blocks, int tiles) {
-    constexpr int ROWS = kRows<LW>;
+// Up to 8 tokens at once; a block as above.
+template <typename T, int LW, int R, int V, int K>
+__global__ void __launch_bounds__(32 * kMaxWarps, kChunkBlocks)
+decode_chunks_kernel(RunsArgs a, int row_blocks, int tiles) {
+    constexpr int ROWS = kRows<LW, R>;
     constexpr int PD = LW * V * 4;       // padded Dk
     constexpr int E = (PD + 31) / 32;    // a lane's elements of k where a warp holds a token
     __shared__ __align__(16) float sk[kTok][PD], sq[kTok][PD];
@@ -301,21 +339,17 @@ decode_runs_kernel(RunsArgs a, int row_blocks, int tiles) {
     bool run = slot >= 0 && slot < a.n_slots;
     const int row0 = rb * tiles * warps * ROWS;
     float *state = a.states + ((long long)(run ? slot : 0) * a.Hv + h) * a.Dv * a.Dk;
-    if (t1 - t0 == 1) {
-        one_token<T, LW, V, VEC>(a, state, n, h, t0, slot, run, row0, tiles);
-        return;
-    }
     const T *vp = static_cast<const T *>(a.v) + (long long)h * a.Dv;
     T *op = a.o ? static_cast<T *>(a.o) + (long long)h * a.Dv : nullptr;
     const int sub = lane % LW, grp = lane / LW;
     const int hk = h / (a.Hv / a.Hk);
     float4 s[R][V];
-    load_rows<LW, V, VEC>(a, state, row0 + warp * ROWS, lane, run, s);
+    load_rows<LW, R, V, K>(a, state, row0 + warp * ROWS, lane, run, s);
 
     for (int tile = 0; tile < tiles; ++tile) {
         const int wrow = row0 + (tile * warps + warp) * ROWS;  // the warp's first row
         if (row0 + tile * warps * ROWS >= a.Dv) break;
-        if (tile) load_rows<LW, V, VEC>(a, state, wrow, lane, true, s);
+        if (tile) load_rows<LW, R, V, K>(a, state, wrow, lane, true, s);
         for (int c0 = t0; c0 < t1; c0 += kTok) {
             const int m = min(kTok, t1 - c0);
             // a run of one chunk keeps its tokens' arrays for all row tiles
@@ -357,8 +391,8 @@ decode_runs_kernel(RunsArgs a, int row_blocks, int tiles) {
                         }
                     }
                     if (lane == 0) {
-                        const float2 gp = gate_pair(g0, g1, a.flags);
-                        al[j] = expf(gp.x);
+                        const float2 gp = decay_pair(g0, g1, a.flags);
+                        al[j] = gp.x;
                         be[j] = gp.y;
                     }
                 }
@@ -399,19 +433,19 @@ decode_runs_kernel(RunsArgs a, int row_blocks, int tiles) {
                         }
                     }
                     const int w = reduce_scatter<2 * kTok, 32>(x, lane), j = w % kTok;
+                    // Gamma_ij; the lane with j = 0 goes on to gamma_i, another to the
+                    // product of the decays behind i
                     float dec = 1.f;
-                    for (int l = j + 1; l <= i; ++l) dec *= al[l];
+                    const bool behind = lane == 1;
+                    const int l0 = behind ? i + 1 : j + 1, l1 = behind ? m : i + 1;
+#pragma unroll
+                    for (int l = 1; l < kTok; ++l)
+                        if (l >= l0 && l < l1) dec *= al[l];
+                    if (behind) tail[i] = dec;
+                    if (lane == 0) gam[i] = dec * al[0];
                     if (lane % 2 == 0 && j <= i) {
                         if (w < kTok) sA[i][j] = be[i] * dec * x[0];
                         else sP[i][j] = dec * x[0];
-                    }
-                    if (lane == 0) {
-                        float g = 1.f;
-                        for (int l = 0; l <= i; ++l) g *= al[l];
-                        gam[i] = g;
-                        g = 1.f;
-                        for (int l = i + 1; l < m; ++l) g *= al[l];
-                        tail[i] = g;
                     }
                 }
                 __syncthreads();
@@ -443,14 +477,18 @@ decode_runs_kernel(RunsArgs a, int row_blocks, int tiles) {
             }
             // the rows' products with k and q
             for (int j = 0; j < m; ++j) {
-                float4 k4[V], q4[V];
+                float2 acc[2 * R];
+                float x[2 * R];
+#pragma unroll
+                for (int i = 0; i < 2 * R; ++i) acc[i] = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    k4[v] = *reinterpret_cast<const float4 *>(&sk[j][4 * (v * LW + sub)]);
-                    q4[v] = *reinterpret_cast<const float4 *>(&sq[j][4 * (v * LW + sub)]);
+                    const float4 k4 = *reinterpret_cast<const float4 *>(&sk[j][4 * (v * LW + sub)]);
+                    const float4 q4 = *reinterpret_cast<const float4 *>(&sq[j][4 * (v * LW + sub)]);
+                    row_dots<R, V>(s, v, k4, q4, acc);
                 }
-                float x[2 * R];
-                row_dots<V>(s, k4, q4, x);
+#pragma unroll
+                for (int i = 0; i < 2 * R; ++i) x[i] = acc[i].x + acc[i].y;
                 const int first = reduce_scatter<2 * R, LW>(x, lane);
                 constexpr int NK = 2 * R > LW ? 2 * R / LW : 1;  // sums left in a lane
 #pragma unroll
@@ -482,54 +520,75 @@ decode_runs_kernel(RunsArgs a, int row_blocks, int tiles) {
             }
             __syncwarp();
             if (a.update || c0 + kTok < t1) {
-                scale_rows<V>(s, gam[m - 1]);
+                scale_rows<R, V>(s, gam[m - 1]);
                 for (int j = 0; j < m; ++j) {
-                    const float4 u4 = *reinterpret_cast<const float4 *>(&su[warp][j][grp * R]);
-                    const float u[R] = {u4.x, u4.y, u4.z, u4.w};
-                    float4 k4[V];
+                    float u[R];
 #pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        k4[v] = *reinterpret_cast<const float4 *>(&sk[j][4 * (v * LW + sub)]);
-                    add_rows<V>(s, u, k4);
+                    for (int r = 0; r < R; ++r) u[r] = su[warp][j][grp * R + r];
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const float4 k4 = *reinterpret_cast<const float4 *>(&sk[j][4 * (v * LW + sub)]);
+                        add_rows<R, V>(s, v, u, k4);
+                    }
                 }
             }
             __syncwarp();
         }
-        if (a.update) store_rows<LW, V, VEC>(a, state, wrow, lane, s);
+        if (a.update) store_rows<LW, R, V, K>(a, state, wrow, lane, s);
     }
 }
 
-template <typename T, int LW, int V>
-cudaError_t launch(const RunsArgs &a, cudaStream_t st) {
-    constexpr int ROWS = kRows<LW>;
-    const int warps = min(kMaxWarps, (a.Dv + ROWS - 1) / ROWS);
-    int tiles = (a.Dv + warps * ROWS - 1) / (warps * ROWS), row_blocks = 1;
-    // few heads: their rows are shared out over more blocks, up to two per SM
-    while (tiles > 1 && (long long)a.N * a.Hv * row_blocks < 148 * 2) {
-        tiles = (tiles + 1) / 2;
-        row_blocks = (a.Dv + tiles * warps * ROWS - 1) / (tiles * warps * ROWS);
+// How a launch covers the value channels: warps per block, row tiles per block, blocks
+// per (sequence, head).  Few heads: their rows are shared out over more blocks, up to
+// two per SM.
+struct Cover {
+    int warps, tiles, row_blocks;
+    unsigned blocks;
+};
+Cover cover(const RunsArgs &a, int rows) {
+    Cover c;
+    c.warps = min(kMaxWarps, (a.Dv + rows - 1) / rows);
+    c.tiles = (a.Dv + c.warps * rows - 1) / (c.warps * rows);
+    c.row_blocks = 1;
+    while (c.tiles > 1 && (long long)a.N * a.Hv * c.row_blocks < 148 * 2) {
+        c.tiles = (c.tiles + 1) / 2;
+        c.row_blocks = (a.Dv + c.tiles * c.warps * rows - 1) / (c.tiles * c.warps * rows);
     }
-    const unsigned blocks = (unsigned)((long long)a.N * a.Hv * row_blocks);
-    if (a.Dk % 4 == 0)
-        decode_runs_kernel<T, LW, V, true><<<blocks, 32 * warps, 0, st>>>(a, row_blocks, tiles);
-    else
-        decode_runs_kernel<T, LW, V, false><<<blocks, 32 * warps, 0, st>>>(a, row_blocks, tiles);
-    return cudaPeekAtLastError();
+    c.blocks = (unsigned)((long long)a.N * a.Hv * c.row_blocks);
+    return c;
 }
 
-template <typename T>
+template <typename T, int K>
 cudaError_t launch_t(const RunsArgs &a, cudaStream_t st) {
-    if (a.Dk <= 16) return launch<T, 4, 1>(a, st);
-    if (a.Dk <= 32) return launch<T, 4, 2>(a, st);
-    if (a.Dk <= 64) return launch<T, 8, 2>(a, st);
-    if (a.Dk <= 128) return launch<T, 16, 2>(a, st);
-    return launch<T, 32, 2>(a, st);
+#define GDN_RUNS(KERNEL, LW, R, V)                                                          \
+    do {                                                                                    \
+        const Cover c = cover(a, kRows<LW, R>);                                             \
+        KERNEL<T, LW, R, V, K><<<c.blocks, 32 * c.warps, 0, st>>>(a, c.row_blocks, c.tiles); \
+    } while (0)
+    if (a.total < 2ll * a.N + 4) {  // fewer than two tokens per sequence on average
+        if (a.Dk <= 16) GDN_RUNS(decode_tokens_kernel, 4, 2, 1);
+        else if (a.Dk <= 32) GDN_RUNS(decode_tokens_kernel, 8, 2, 1);
+        else if (a.Dk <= 64) GDN_RUNS(decode_tokens_kernel, 8, 2, 2);
+        else if (a.Dk <= 128) GDN_RUNS(decode_tokens_kernel, 16, 2, 2);
+        else GDN_RUNS(decode_tokens_kernel, 32, 2, 2);
+    } else {
+        if (a.Dk <= 16) GDN_RUNS(decode_chunks_kernel, 4, 4, 1);
+        else if (a.Dk <= 32) GDN_RUNS(decode_chunks_kernel, 4, 4, 2);
+        else if (a.Dk <= 64) GDN_RUNS(decode_chunks_kernel, 4, 2, 4);
+        else if (a.Dk <= 128) GDN_RUNS(decode_chunks_kernel, 8, 2, 4);
+        else GDN_RUNS(decode_chunks_kernel, 16, 2, 4);
+    }
+#undef GDN_RUNS
+    return cudaPeekAtLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_decode_runs(const RunsArgs &a, bool bf16, cudaStream_t st) {
-    return bf16 ? launch_t<__nv_bfloat16>(a, st) : launch_t<float>(a, st);
+    const bool full = a.Dk == 16 || a.Dk == 32 || a.Dk == 64 || a.Dk == 128 || a.Dk == 256;
+    if (a.Dk % 4) return bf16 ? launch_t<__nv_bfloat16, kAny>(a, st) : launch_t<float, kAny>(a, st);
+    if (!full) return bf16 ? launch_t<__nv_bfloat16, kVec>(a, st) : launch_t<float, kVec>(a, st);
+    return bf16 ? launch_t<__nv_bfloat16, kFull>(a, st) : launch_t<float, kFull>(a, st);
 }
 
 }  // namespace gdn
