@@ -478,57 +478,75 @@ def decode_step(q, k, v, log_alpha, beta, S, out=None, l2norm_qk: bool = False,
 GDN_FLAG_READ_ONLY = 4
 
 
-def _rows(t: torch.Tensor, name: str, dtype, device):
-    """Pointer and token stride of [tokens, ...] whose tokens are dense."""
+def _cuda(t, name: str) -> int:
+    """Index of the CUDA device that tensor ``t`` is on."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise GdnError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    return t.get_device()
+
+
+def _dense(t, name: str, dtype, dev: int) -> int:
+    """Pointer of a dense tensor on device ``dev``."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise GdnError(f"{name} must be a tensor on CUDA device {dev}")
+    if t.dtype is not dtype:
         raise GdnError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise GdnError(f"{name} is on {t.device}, expected {device}")
-    width, shape, strides = 1, t.shape, t.stride()
+    if not t.is_contiguous():
+        raise GdnError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, name: str, dtype, dev: int):
+    """Pointer and token stride of [tokens, ...] whose tokens are dense."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise GdnError(f"{name} must be a tensor on CUDA device {dev}")
+    if t.dtype is not dtype:
+        raise GdnError(f"{name} must be {dtype}, got {t.dtype}")
+    shape, strides = t.shape, t.stride()
+    width = 1
     for i in range(len(shape) - 1, 0, -1):
-        if shape[i] != 1 and strides[i] != width:
-            raise GdnError(f"{name}: the channels of a token must be contiguous")
-        width *= shape[i]
+        n = shape[i]
+        if n != 1:
+            if strides[i] != width:
+                raise GdnError(f"{name}: the channels of a token must be contiguous")
+            width *= n
     return t.data_ptr(), strides[0] if shape[0] > 1 else max(width, 1)
 
 
-def _param(t: torch.Tensor, name: str, shape, dtype, device):
+def _param(t, name: str, shape, dtype, dev: int):
     if t.shape != shape:
         raise GdnError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.dtype != torch.float32 and t.dtype != dtype:
-        raise GdnError(f"{name} must be float32 or {dtype}, got {t.dtype}")
-    return _dev(t, name, None, device)
+    return _dense(t, name, dtype if t.dtype is dtype else torch.float32, dev)
 
 
-def _call(device, f, *args):
-    """f(*args, stream) with ``device`` current."""
-    if device.index == torch.cuda.current_device():
-        return f(*args, _stream_ptr(device))
-    with torch.cuda.device(device):
-        return f(*args, _stream_ptr(device))
+def _call(dev: int, f, *args):
+    """f(*args, stream of device ``dev``) with that device current."""
+    if dev == torch._C._cuda_getDevice():
+        return f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    with torch.cuda.device(dev):
+        return f(*args, torch._C._cuda_getCurrentRawStream(dev))
 
 
-def _scratch(need: int, workspace, device):
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    return _dev(workspace, "workspace", None, device), workspace.numel() * workspace.element_size()
+def _scratch(need: int, workspace, like, dev: int):
+    if workspace is None:
+        return like.new_empty(max(need, 16), dtype=torch.uint8).data_ptr(), max(need, 16)
+    return (_dense(workspace, "workspace", workspace.dtype, dev),
+            workspace.numel() * workspace.element_size())
 
 
-def _sequences(cu_seqlens, slots, total, device):
+def _sequences(cu_seqlens, slots, total, dev: int):
     """Pointers of the offsets and slots (int32 device tensors) and the number of sequences."""
     cu = sl = None
     N = total
     if cu_seqlens is not None:
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        cu = _dense(cu_seqlens, "cu_seqlens", torch.int32, dev)
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
             raise GdnError("cu_seqlens must hold N + 1 offsets")
-        N = cu_seqlens.numel() - 1
-        cu = _dev(cu_seqlens, "cu_seqlens", torch.int32, device)
+        N = cu_seqlens.shape[0] - 1
     if slots is not None:
+        sl = _dense(slots, "slots", torch.int32, dev)
         if slots.shape != (N,):
             raise GdnError("slots must hold one slot per sequence")
-        sl = _dev(slots, "slots", torch.int32, device)
     return cu, sl, N
 
 
@@ -557,47 +575,54 @@ def decode_runs(q, k, v, log_alpha, beta, states, slots=None, cu_seqlens=None, o
         raise GdnError("q, k must be [total,Hk,Dk] and v [total,Hv,Dv]")
     total, Hk, Dk = k.shape
     _, Hv, Dv = v.shape
-    dev, dtype = k.device, k.dtype
+    dev, dtype = _cuda(k, "k"), k.dtype
     code = _dtype_code(k)
-    if log_alpha.shape != (total, Hv) or beta.shape != (total, Hv):
+    gates = (total, Hv)
+    if log_alpha.shape != gates or beta.shape != gates:
         raise GdnError("log_alpha and beta must be [total,Hv]")
     if states.dim() != 4 or states.shape[1:] != (Hv, Dv, Dk):
         raise GdnError("states must be [n_slots,Hv,Dv,Dk]")
     if Hk == 0 or Hv % Hk:
         raise GdnError("Hv must be a multiple of Hk")
+    n_slots = states.shape[0]
     kp, ks = _rows(k, "k", dtype, dev)
     qp, qs = _rows(q, "q", dtype, dev) if q is not None else (None, 0)
     vp, vs = _rows(v, "v", dtype, dev)
     ap, as_ = _rows(log_alpha, "log_alpha", torch.float32, dev)
     bp, bs = _rows(beta, "beta", torch.float32, dev)
     cu, sl, N = _sequences(cu_seqlens, slots, total, dev)
-    if slots is None and N > states.shape[0]:
+    if slots is None and N > n_slots:
         raise GdnError("without slots, states must hold one state per sequence")
     o = op = None
     if want_output:
-        o = out if out is not None else torch.empty((total, Hv, Dv), dtype=dtype, device=dev)
+        o = out if out is not None else k.new_empty((total, Hv, Dv))
         if o.shape != (total, Hv, Dv):
             raise GdnError("out must be [total,Hv,Dv]")
-        op = _dev(o, "out", dtype, dev)
+        op = _dense(o, "out", dtype, dev)
     flags = _flags(l2norm_qk, gate_logits) | (0 if update else GDN_FLAG_READ_ONLY)
-    st = _call(dev, LIB.gdn_decode_runs, qp, kp, vp, ap, bp,
-               _dev(states, "states", torch.float32, dev), sl, cu, op, N, total, Hk, Hv, Dk, Dv,
-               states.shape[0], qs, ks, vs, as_, bs, code, flags)
-    _check(st, "gdn_decode_runs")
+    _check(_call(dev, LIB.gdn_decode_runs, qp, kp, vp, ap, bp,
+                 _dense(states, "states", torch.float32, dev), sl, cu, op, N, total, Hk, Hv, Dk,
+                 Dv, n_slots, qs, ks, vs, as_, bs, code, flags), "gdn_decode_runs")
     return o
 
 
 def _parts(tensors, splits, total, dtype, dev, name):
     """Pointers, strides and channel offsets (ctypes arrays) of the parts of y or dy."""
-    n = len(tensors)
-    ptrs, strides = (ctypes.c_void_p * n)(), (ctypes.c_longlong * n)()
-    begin = (ctypes.c_int * (n + 1))()
-    for i, (t, c) in enumerate(zip(tensors, splits)):
+    ptrs, strides, begin = [], [], [0]
+    for t, c in zip(tensors, splits):
         if t.shape != (total, c):
             raise GdnError(f"{name} must be [total,C], split as the channels are")
-        ptrs[i], strides[i] = _rows(t, name, dtype, dev)
-        begin[i + 1] = begin[i] + c
-    return ptrs, strides, begin
+        p, s = _rows(t, name, dtype, dev)
+        ptrs.append(p)
+        strides.append(s)
+        begin.append(begin[-1] + c)
+    n = len(ptrs)
+    return _PTRS[n](*ptrs), _LONGS[n](*strides), _INTS[n + 1](*begin)
+
+
+_PTRS = [ctypes.c_void_p * n for n in range(4)]
+_LONGS = [ctypes.c_longlong * n for n in range(4)]
+_INTS = [ctypes.c_int * n for n in range(5)]
 
 
 def short_conv_fwd(x, weight, bias=None, cu_seqlens=None, states=None, slots=None, silu: bool = True,
@@ -617,13 +642,13 @@ def short_conv_fwd(x, weight, bias=None, cu_seqlens=None, states=None, slots=Non
         raise GdnError("x must be [total,C] and weight [C,W]")
     total, C = x.shape
     W = weight.shape[1]
-    dev, dtype = x.device, x.dtype
+    dev, dtype = _cuda(x, "x"), x.dtype
     code = _dtype_code(x)
     xp, xs = _rows(x, "x", dtype, dev)
     wp = _param(weight, "weight", (C, W), dtype, dev)
     bp = None
     if bias is not None:
-        if bias.dtype != weight.dtype:
+        if bias.dtype is not weight.dtype:
             raise GdnError("bias and weight must have one type")
         bp = _param(bias, "bias", (C,), dtype, dev)
     if slots is not None and states is None:
@@ -636,12 +661,12 @@ def short_conv_fwd(x, weight, bias=None, cu_seqlens=None, states=None, slots=Non
         n_slots = states.shape[0]
         if slots is None and N > n_slots:
             raise GdnError("without slots, states must hold one state per sequence")
-        sp = _dev(states, "states", dtype, dev)
+        sp = _dense(states, "states", dtype, dev)
     widths = [C] if splits is None else list(splits)
     if not 1 <= len(widths) <= 3 or sum(widths) != C or min(widths) <= 0:
         raise GdnError("splits must be one to three widths that sum to C")
     if out is None:
-        ys = tuple(torch.empty((total, c), dtype=dtype, device=dev) for c in widths)
+        ys = tuple([x.new_empty((total, c)) for c in widths])
     else:
         ys = (out,) if splits is None else tuple(out)
         if len(ys) != len(widths):
@@ -668,24 +693,25 @@ def short_conv_bwd(dy, x, weight, bias=None, cu_seqlens=None, silu: bool = True,
         raise GdnError("x must be [total,C] and weight [C,W]")
     total, C = x.shape
     W = weight.shape[1]
-    dev, dtype = x.device, x.dtype
+    dev, dtype = _cuda(x, "x"), x.dtype
     code = _dtype_code(x)
     xp, xs = _rows(x, "x", dtype, dev)
     wp = _param(weight, "weight", (C, W), dtype, dev)
     bp = None
     if bias is not None:
-        if bias.dtype != weight.dtype:
+        if bias.dtype is not weight.dtype:
             raise GdnError("bias and weight must have one type")
         bp = _param(bias, "bias", (C,), dtype, dev)
     cu, _, N = _sequences(cu_seqlens, None, total, dev)
     dys = (dy,) if isinstance(dy, torch.Tensor) else tuple(dy)
-    if not 1 <= len(dys) <= 3 or any(d.dim() != 2 for d in dys) or sum(d.shape[1] for d in dys) != C:
+    widths = [d.shape[1] for d in dys if d.dim() == 2]
+    if not 1 <= len(dys) <= 3 or len(widths) != len(dys) or sum(widths) != C:
         raise GdnError("dy must be [total,C] or up to three arrays of C channels in all")
-    ptrs, strides, begin = _parts(dys, [d.shape[1] for d in dys], total, dtype, dev, "dy")
-    dx = torch.empty((total, C), dtype=dtype, device=dev)
-    dw = torch.empty((C, W), dtype=torch.float32, device=dev)
-    db = torch.empty((C,), dtype=torch.float32, device=dev) if bias is not None else None
-    ws, nbytes = _scratch(int(LIB.gdn_short_conv_bwd_workspace_size(total, C, W)), workspace, dev)
+    ptrs, strides, begin = _parts(dys, widths, total, dtype, dev, "dy")
+    dx = x.new_empty((total, C))
+    dw = x.new_empty((C, W), dtype=torch.float32)
+    db = x.new_empty((C,), dtype=torch.float32) if bias is not None else None
+    ws, nbytes = _scratch(LIB.gdn_short_conv_bwd_workspace_size(total, C, W), workspace, x, dev)
     st = _call(dev, LIB.gdn_short_conv_bwd, ptrs, strides, begin, len(dys), xp, wp, bp, cu,
                dx.data_ptr(), dw.data_ptr(), db.data_ptr() if db is not None else None, N, total,
                C, W, xs, int(silu), code, _dtype_code(weight), ws, nbytes)
@@ -698,9 +724,9 @@ def _norm_rows(t, name, shape, dtype, dev):
     of a token where there are three axes or more, the axes before it the tokens."""
     if t.shape != shape:
         raise GdnError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.dim() == 1:
+    if len(shape) == 1:
         t = t.unsqueeze(0)
-    elif t.dim() > 3:
+    elif len(shape) > 3:
         try:
             t = t.view(-1, *t.shape[-2:])
         except RuntimeError:
@@ -730,7 +756,7 @@ def rms_norm_fwd(x, weight, residual=None, gate=None, eps: float = 1e-6, quant=N
     [..., D / group] float32 per row or per 128 columns, the value being y * scale.
     ``out`` / ``h_out``: arrays for y and h (h_out may be the residual itself).
     """
-    shape, dev, dtype = x.shape, x.device, x.dtype
+    shape, dev, dtype = x.shape, _cuda(x, "x"), x.dtype
     code = _dtype_code(x)
     tokens, heads, D = _norm_sizes(shape)
     xp, xs = _norm_rows(x, "x", shape, dtype, dev)
@@ -743,20 +769,20 @@ def rms_norm_fwd(x, weight, residual=None, gate=None, eps: float = 1e-6, quant=N
     if quant == "group" and D % 128:
         raise GdnError("groups of 128 columns need D to be a multiple of 128")
     ytype = dtype if quant is None else torch.float8_e4m3fn
-    y = out if out is not None else torch.empty(shape, dtype=ytype, device=dev)
+    y = out if out is not None else x.new_empty(shape, dtype=ytype)
     if y.shape != shape:
         raise GdnError("out must be shaped like x")
-    yp = _dev(y, "out", ytype, dev)
+    yp = _dense(y, "out", ytype, dev)
     scale = sc = None
     if group:
-        scale = torch.empty(shape[:-1] + (D // group,), dtype=torch.float32, device=dev)
+        scale = x.new_empty(shape[:-1] + (D // group,), dtype=torch.float32)
         sc = scale.data_ptr()
     h = hp = None
     if residual is not None:
-        h = h_out if h_out is not None else torch.empty(shape, dtype=dtype, device=dev)
+        h = h_out if h_out is not None else x.new_empty(shape)
         if h.shape != shape:
             raise GdnError("h_out must be shaped like x")
-        hp = _dev(h, "h_out", dtype, dev)
+        hp = _dense(h, "h_out", dtype, dev)
     elif h_out is not None:
         raise GdnError("h_out without residual")
     st = _call(dev, LIB.gdn_rms_norm_fwd, xp, wp, rp, gp, yp, sc, hp, tokens, heads, D, group, xs,
@@ -777,7 +803,7 @@ def rms_norm_bwd(dy, x, weight, gate=None, d_res=None, eps: float = 1e-6, worksp
     h is used again.  dx, in x's type, is the gradient of both x and the residual;
     dweight [D] is float32; dgate is None without gate.
     """
-    shape, dev, dtype = x.shape, x.device, x.dtype
+    shape, dev, dtype = x.shape, _cuda(x, "x"), x.dtype
     code = _dtype_code(x)
     tokens, heads, D = _norm_sizes(shape)
     xp, xs = _norm_rows(x, "x", shape, dtype, dev)
@@ -785,10 +811,10 @@ def rms_norm_bwd(dy, x, weight, gate=None, d_res=None, eps: float = 1e-6, worksp
     wp = _param(weight, "weight", (D,), dtype, dev)
     gp, gs = _norm_rows(gate, "gate", shape, dtype, dev) if gate is not None else (None, 0)
     dp, ds = _norm_rows(d_res, "d_res", shape, dtype, dev) if d_res is not None else (None, 0)
-    dx = torch.empty(shape, dtype=dtype, device=dev)
-    dw = torch.empty((D,), dtype=torch.float32, device=dev)
-    dgate = torch.empty(shape, dtype=dtype, device=dev) if gate is not None else None
-    ws, nbytes = _scratch(int(LIB.gdn_rms_norm_bwd_workspace_size(tokens, heads, D)), workspace, dev)
+    dx = x.new_empty(shape)
+    dw = x.new_empty((D,), dtype=torch.float32)
+    dgate = x.new_empty(shape) if gate is not None else None
+    ws, nbytes = _scratch(LIB.gdn_rms_norm_bwd_workspace_size(tokens, heads, D), workspace, x, dev)
     st = _call(dev, LIB.gdn_rms_norm_bwd, yp, xp, wp, gp, dp, dx.data_ptr(), dw.data_ptr(),
                dgate.data_ptr() if dgate is not None else None, tokens, heads, D, ys, xs, gs, ds,
                eps, code, _dtype_code(weight), ws, nbytes)

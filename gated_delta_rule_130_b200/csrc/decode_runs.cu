@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kTok = 8;       // tokens taken at once
 constexpr int kMaxWarps = 8;  // per block
-constexpr int kTokenBlocks = 4, kChunkBlocks = 3;  // blocks per SM
+constexpr int kTokenBlocks = 5, kChunkBlocks = 3;  // blocks per SM
 
 // Sums of NV values per lane over LW neighbouring lanes: while lanes and values
 // last, each step hands half of the values to the partner lane; afterwards lane l
@@ -566,10 +566,13 @@ cudaError_t launch_t(const RunsArgs &a, cudaStream_t st) {
         KERNEL<T, LW, R, V, K><<<c.blocks, 32 * c.warps, 0, st>>>(a, c.row_blocks, c.tiles); \
     } while (0)
     if (a.total < 2ll * a.N + 4) {  // fewer than two tokens per sequence on average
-        if (a.Dk <= 16) GDN_RUNS(decode_tokens_kernel, 4, 2, 1);
-        else if (a.Dk <= 32) GDN_RUNS(decode_tokens_kernel, 8, 2, 1);
-        else if (a.Dk <= 64) GDN_RUNS(decode_tokens_kernel, 8, 2, 2);
-        else if (a.Dk <= 128) GDN_RUNS(decode_tokens_kernel, 16, 2, 2);
+        // (a row over as many lanes as it has float4, four rows per lane group: 92.9 us on
+        // 256 sequences of 16 heads of 128 x 128; 16 lanes of two float4 and two rows
+        // 101.6 us, 8 lanes of four 129.8 us)
+        if (a.Dk <= 16) GDN_RUNS(decode_tokens_kernel, 4, 4, 1);
+        else if (a.Dk <= 32) GDN_RUNS(decode_tokens_kernel, 8, 4, 1);
+        else if (a.Dk <= 64) GDN_RUNS(decode_tokens_kernel, 16, 4, 1);
+        else if (a.Dk <= 128) GDN_RUNS(decode_tokens_kernel, 32, 4, 1);
         else GDN_RUNS(decode_tokens_kernel, 32, 2, 2);
     } else {
         if (a.Dk <= 16) GDN_RUNS(decode_chunks_kernel, 4, 4, 1);
