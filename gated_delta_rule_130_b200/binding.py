@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from itertools import accumulate
 
 import torch
 
@@ -502,7 +503,10 @@ def _rows(t, name: str, dtype, dev: int):
         raise GdnError(f"{name} must be a tensor on CUDA device {dev}")
     if t.dtype is not dtype:
         raise GdnError(f"{name} must be {dtype}, got {t.dtype}")
-    shape, strides = t.shape, t.stride()
+    shape = t.shape
+    if shape[0] > 1 and t.is_contiguous():
+        return t.data_ptr(), t.stride(0)
+    strides = t.stride()
     width = 1
     for i in range(len(shape) - 1, 0, -1):
         n = shape[i]
@@ -665,13 +669,16 @@ def short_conv_fwd(x, weight, bias=None, cu_seqlens=None, states=None, slots=Non
     widths = [C] if splits is None else list(splits)
     if not 1 <= len(widths) <= 3 or sum(widths) != C or min(widths) <= 0:
         raise GdnError("splits must be one to three widths that sum to C")
+    n = len(widths)
     if out is None:
         ys = tuple([x.new_empty((total, c)) for c in widths])
+        ptrs, strides = _PTRS[n](*[y.data_ptr() for y in ys]), _LONGS[n](*widths)
+        begin = _INTS[n + 1](0, *accumulate(widths))
     else:
         ys = (out,) if splits is None else tuple(out)
-        if len(ys) != len(widths):
+        if len(ys) != n:
             raise GdnError("out must hold one array per split")
-    ptrs, strides, begin = _parts(ys, widths, total, dtype, dev, "out")
+        ptrs, strides, begin = _parts(ys, widths, total, dtype, dev, "out")
     st = _call(dev, LIB.gdn_short_conv_fwd, xp, wp, bp, sp, sl, cu, ptrs, strides, begin,
                len(widths), N, total, C, W, n_slots, xs, int(silu), code, _dtype_code(weight))
     _check(st, "gdn_short_conv_fwd")

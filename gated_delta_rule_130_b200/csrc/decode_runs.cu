@@ -321,6 +321,7 @@ decode_chunks_kernel(RunsArgs a, int row_blocks, int tiles) {
     constexpr int ROWS = kRows<LW, R>;
     constexpr int PD = LW * V * 4;       // padded Dk
     constexpr int E = (PD + 31) / 32;    // a lane's elements of k where a warp holds a token
+    constexpr int VI = ROWS * kTok / 32;  // a lane's share of a warp's rows and tokens
     __shared__ __align__(16) float sk[kTok][PD], sq[kTok][PD];
     // tm[0]: T with u = T r, tm[1]: M with o = gamma b + M r  (r = v - gamma a)
     __shared__ float sA[kTok][kTok], sP[kTok][kTok], tm[2][kTok][kTok];
@@ -352,6 +353,13 @@ decode_chunks_kernel(RunsArgs a, int row_blocks, int tiles) {
         if (tile) load_rows<LW, R, V, K>(a, state, wrow, lane, true, s);
         for (int c0 = t0; c0 < t1; c0 += kTok) {
             const int m = min(kTok, t1 - c0);
+            float vv[VI];  // v of the warp's rows, needed last
+#pragma unroll
+            for (int i = 0; i < VI; ++i) {
+                const int j = (lane + 32 * i) / ROWS, row = (lane + 32 * i) % ROWS;
+                vv[i] = run && j < m && wrow + row < a.Dv
+                            ? to_f32(vp[(c0 + j) * a.v_stride + wrow + row]) : 0.f;
+            }
             // a run of one chunk keeps its tokens' arrays for all row tiles
             if (tile == 0 || t1 - t0 > kTok) {
                 if (tile || c0 > t0) __syncthreads();  // the arrays are written again
@@ -500,10 +508,10 @@ decode_chunks_kernel(RunsArgs a, int row_blocks, int tiles) {
             if (tile == 0 || t1 - t0 > kTok) __syncthreads();  // T and M are there
             else __syncwarp();
             // each row's r, then its outputs and corrections
-            for (int at = lane; at < ROWS * m; at += 32) {
-                const int j = at / ROWS, row = at % ROWS;
-                const float v = wrow + row < a.Dv ? to_f32(vp[(c0 + j) * a.v_stride + wrow + row]) : 0.f;
-                ra[warp][j][row] = v - gam[j] * ra[warp][j][row];
+#pragma unroll
+            for (int i = 0; i < VI; ++i) {
+                const int j = (lane + 32 * i) / ROWS, row = (lane + 32 * i) % ROWS;
+                if (j < m) ra[warp][j][row] = vv[i] - gam[j] * ra[warp][j][row];
             }
             __syncwarp();
             for (int at = lane; at < ROWS * m; at += 32) {

@@ -323,25 +323,23 @@ conv_few(ConvArgs a, unsigned ctiles) {
     load_vec<T, VEC>(x + t * a.x_stride, now);
     load_weights<T, VEC, W>(a, cc, w, b);
 
-    int n = t, start = t, end = t + 1;
+    int n = t, start = t, end = t + 1, slot = -1;
     if (a.cu) {
-        n = (int)((long long)t * a.N / a.total);  // where the sequences are equally long
+        n = (int)((long long)t * a.N / a.total);  // right where the sequences are equally long
         start = a.cu[n];
         end = a.cu[n + 1];
-        if (start > t || end <= t) {
-            n = seq_of(a.cu, a.N, t, lane);
-            start = a.cu[n];
-            end = a.cu[n + 1];
-        }
-        if (start < 0 || start > t || end <= t || end > a.total) return;  // in no sequence
     }
+    if (a.states) slot = a.slots ? a.slots[n] : n;
+    if (start > t || end <= t) {
+        n = seq_of(a.cu, a.N, t, lane);
+        start = a.cu[n];
+        end = a.cu[n + 1];
+        if (a.states) slot = a.slots ? a.slots[n] : n;
+    }
+    if (start < 0 || start > t || end <= t || end > a.total) return;  // in no sequence
     const int pos = t - start;
     if (pos > 0 && pos < W - 1) return;  // taken with the sequence's first token
-    int slot = -1;
-    if (a.states) {
-        slot = a.slots ? a.slots[n] : n;
-        if (slot >= a.n_slots) slot = -1;
-    }
+    if (slot >= a.n_slots) slot = -1;
     const bool padding = a.states && slot < 0;
     T *held = a.states && !padding
                   ? static_cast<T *>(a.states) + (long long)slot * (W - 1) * a.C + cc : nullptr;
