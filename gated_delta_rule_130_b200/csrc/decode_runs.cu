@@ -20,14 +20,13 @@
 // A warp holds its rows in registers, LW lanes per row with V float4 each; k and q
 // stand in shared memory as float32, already normalised.  Everything is float32: the
 // state is carried over thousands of steps.
-#include "common.cuh"
-#include "kernels.h"
+#include "runs_common.cuh"
 
 namespace gdn {
 
 namespace {
 
-constexpr int kTok = 8;       // tokens taken at once
+constexpr int kTok = kRunTokens;
 constexpr int kMaxWarps = 8;  // per block
 constexpr int kTokenBlocks = 5, kChunkBlocks = 3;  // blocks per SM
 
@@ -144,13 +143,6 @@ __device__ __forceinline__ void add_rows(float4 (&s)[R][V], int v, const float (
     }
 }
 
-// The decay and the write strength of a token as the recurrence uses them; with logits
-// alpha = exp(-softplus(x)) = 1 / (1 + e^x).
-__device__ __forceinline__ float2 decay_pair(float la, float be, unsigned flags) {
-    if (flags & kFlagGateLogits) return make_float2(sigmoid(-la), sigmoid(be));
-    return make_float2(expf(la), be);
-}
-
 // A warp's rows of the state from wrow on, zero from Dv on.
 template <int LW, int R, int V, int K>
 __device__ __forceinline__ void load_rows(const RunsArgs &a, const float *state, int wrow, int lane,
@@ -185,15 +177,6 @@ __device__ __forceinline__ void store_rows(const RunsArgs &a, float *state, int 
         for (int v = 0; v < V; ++v)
             if (wrow + lane / LW * R + r < a.Dv)
                 store_state<K>(p + r * Dk, 4 * (v * LW + lane % LW), Dk, s[r][v]);
-}
-
-// Whether an earlier sequence with tokens names this slot (seen by every lane that
-// calls with its own share of the sequences).
-__device__ __forceinline__ int slot_taken(const RunsArgs &a, int n, int slot, int from, int step) {
-    int taken = 0;
-    for (int i = from; i < n; i += step)
-        if (a.slots[i] == slot) taken |= !a.cu || a.cu[i] < a.cu[i + 1];
-    return taken;
 }
 
 // Token by token: every warp for itself, k, q and their norms in registers and no
@@ -566,6 +549,10 @@ Cover cover(const RunsArgs &a, int rows) {
     return c;
 }
 
+// Two tokens per sequence or more on average (a batch's rows behind its last sequence
+// count too): up to 8 tokens at once, else token by token.
+bool many_tokens(const RunsArgs &a) { return a.total >= 2ll * a.N + 4; }
+
 template <typename T, int K>
 cudaError_t launch_t(const RunsArgs &a, cudaStream_t st) {
 #define GDN_RUNS(KERNEL, LW, R, V)                                                          \
@@ -573,7 +560,7 @@ cudaError_t launch_t(const RunsArgs &a, cudaStream_t st) {
         const Cover c = cover(a, kRows<LW, R>);                                             \
         KERNEL<T, LW, R, V, K><<<c.blocks, 32 * c.warps, 0, st>>>(a, c.row_blocks, c.tiles); \
     } while (0)
-    if (a.total < 2ll * a.N + 4) {  // fewer than two tokens per sequence on average
+    if (!many_tokens(a)) {
         // (a row over as many lanes as it has float4, four rows per lane group: 92.9 us on
         // 256 sequences of 16 heads of 128 x 128; 16 lanes of two float4 and two rows
         // 101.6 us, 8 lanes of four 129.8 us)
@@ -596,6 +583,7 @@ cudaError_t launch_t(const RunsArgs &a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_decode_runs(const RunsArgs &a, bool bf16, cudaStream_t st) {
+    if (bf16 && many_tokens(a) && runs_tc_supported(a)) return launch_decode_runs_tc(a, st);
     const bool full = a.Dk == 16 || a.Dk == 32 || a.Dk == 64 || a.Dk == 128 || a.Dk == 256;
     if (a.Dk % 4) return bf16 ? launch_t<__nv_bfloat16, kAny>(a, st) : launch_t<float, kAny>(a, st);
     if (!full) return bf16 ? launch_t<__nv_bfloat16, kVec>(a, st) : launch_t<float, kVec>(a, st);

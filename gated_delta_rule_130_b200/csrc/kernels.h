@@ -184,6 +184,10 @@ struct RunsArgs {
     bool update;
 };
 cudaError_t launch_decode_runs(const RunsArgs &a, bool bf16, cudaStream_t st);
+// The same for bf16 runs of several tokens, Dk = 64 or 128, on the tensor cores:
+// decode_runs_tc.cu.
+bool runs_tc_supported(const RunsArgs &a);
+cudaError_t launch_decode_runs_tc(const RunsArgs &a, cudaStream_t st);
 
 // Short causal depthwise convolution: short_conv.cu.  The channels of y (dy) lie
 // in up to kConvParts arrays, part p holding the channels [begin[p], begin[p + 1]).
