@@ -307,8 +307,8 @@ decode_chunks_kernel(RunsArgs a, int row_blocks, int tiles) {
     constexpr int VI = ROWS * kTok / 32;  // a lane's share of a warp's rows and tokens
     __shared__ __align__(16) float sk[kTok][PD], sq[kTok][PD];
     // tm[0]: T with u = T r, tm[1]: M with o = gamma b + M r  (r = v - gamma a)
-    __shared__ float sA[kTok][kTok], sP[kTok][kTok], tm[2][kTok][kTok];
-    __shared__ float al[kTok], be[kTok], gam[kTok], tail[kTok];
+    __shared__ __align__(16) float sA[kTok][kTok], sP[kTok][kTok], al[kTok];
+    __shared__ float tm[2][kTok][kTok], be[kTok], gam[kTok], tail[kTok];
     // per warp and token, a row per column: a then r, b, the corrections
     __shared__ __align__(16) float ra[kMaxWarps][kTok][ROWS], rb_[kMaxWarps][kTok][ROWS];
     __shared__ __align__(16) float su[kMaxWarps][kTok][ROWS];
@@ -424,47 +424,18 @@ decode_chunks_kernel(RunsArgs a, int row_blocks, int tiles) {
                         }
                     }
                     const int w = reduce_scatter<2 * kTok, 32>(x, lane), j = w % kTok;
-                    // Gamma_ij; the lane with j = 0 goes on to gamma_i, another to the
-                    // product of the decays behind i
-                    float dec = 1.f;
-                    const bool behind = lane == 1;
-                    const int l0 = behind ? i + 1 : j + 1, l1 = behind ? m : i + 1;
-#pragma unroll
-                    for (int l = 1; l < kTok; ++l)
-                        if (l >= l0 && l < l1) dec *= al[l];
-                    if (behind) tail[i] = dec;
-                    if (lane == 0) gam[i] = dec * al[0];
+                    float dk[kTok];
+                    load8(al, dk);
+                    const float dec = decay_between(dk, j + 1, i + 1);  // Gamma_ij
+                    if (lane == 0) gam[i] = decay_between(dk, 0, i + 1);
+                    if (lane == 1) tail[i] = decay_between(dk, i + 1, m);
                     if (lane % 2 == 0 && j <= i) {
                         if (w < kTok) sA[i][j] = be[i] * dec * x[0];
                         else sP[i][j] = dec * x[0];
                     }
                 }
                 __syncthreads();
-                if (warp == 0) {  // column j of T = (I + A)^-1 diag(beta), then of M = P T
-                    const int j = lane % kTok;
-                    float x[kTok];
-#pragma unroll
-                    for (int i = 0; i < kTok; ++i) {
-                        x[i] = i == j ? 1.f : 0.f;
-#pragma unroll
-                        for (int l = 0; l < i; ++l)
-                            if (i < m && l >= j) x[i] -= sA[i][l] * x[l];
-                    }
-                    const float b = j < m ? be[j] : 0.f;
-                    for (int i = lane / kTok; i < m; i += 32 / kTok) {
-                        float p = 0.f, xi = 0.f;
-#pragma unroll
-                        for (int l = 0; l < kTok; ++l)
-                            if (l >= j && l <= i) {
-                                p += sP[i][l] * x[l];
-                                if (l == i) xi = x[l];
-                            }
-                        if (j <= i) {
-                            tm[0][i][j] = b * xi;
-                            tm[1][i][j] = b * p;
-                        }
-                    }
-                }
+                if (warp == 0) solve_tokens(sA, sP, be, m, lane, tm);
             }
             // the rows' products with k and q
             for (int j = 0; j < m; ++j) {

@@ -72,11 +72,16 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
 decode_chunks_tc_kernel(RunsArgs a, int row_blocks) {
     constexpr int DK = 16 * KS, LD = DK + 8;  // rows 16 bytes apart in their banks
     __shared__ __align__(16) __nv_bfloat16 tok[2][kTok][LD];  // k, q, channels as said above
-    __shared__ __align__(16) float tm[2][kTok][kTok];  // T and M, rows of later tokens
-    __shared__ float sA[kTok][kTok], sP[kTok][kTok];
-    // per token: decay, write strength, 1 / |k|, 1 / |q|; gamma / |k|, gamma / |q|, and
-    // the decays behind it / |k|; last: gamma of all
-    __shared__ float al[kTok], be[kTok], nk[kTok], nq[kTok], ga[kTok], gb[kTok], cf[kTok], gall;
+    // decay and write strength per token
+    __shared__ __align__(16) float al[kTok], be[kTok];
+    // formed by warp 0
+    struct __align__(16) Own {
+        float A[kTok][kTok], P[kTok][kTok], tm[2][kTok][kTok];  // tm: T and M
+        float nk[kTok], nq[kTok];                // 1 / |k|, 1 / |q|
+        float ga[kTok], gb[kTok], cf[kTok];      // gamma / |k|, gamma / |q|, the decays behind / |k|
+    };
+    __shared__ Own my;
+    __shared__ float gall;  // the product of the decays
 
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int g = lane / 4, t = lane % 4;
@@ -163,60 +168,37 @@ decode_chunks_tc_kernel(RunsArgs a, int row_blocks) {
                 mma16(cq, left, b[2], b[3]);
             }
             if (g / 2 == t) {
-                nk[g] = a.flags & kFlagL2Norm ? rsqrtf((g % 2 ? ck[1] : ck[0]) + kNormEps) : 1.f;
-                nq[g] = a.flags & kFlagL2Norm ? rsqrtf((g % 2 ? cq[3] : cq[2]) + kNormEps) : 1.f;
+                my.nk[g] = a.flags & kFlagL2Norm ? rsqrtf((g % 2 ? ck[1] : ck[0]) + kNormEps) : 1.f;
+                my.nq[g] = a.flags & kFlagL2Norm ? rsqrtf((g % 2 ? cq[3] : cq[2]) + kNormEps) : 1.f;
             }
+            float dk[kTok];
+            load8(al, dk);
             __syncwarp();
+            const float nkg = my.nk[g], nqg = my.nq[g];
+            // Gamma_gj and A_gj, P_gj of j = 2t + 1, then of 2t
+            float dec = decay_between(dk, 2 * t + 2, g + 1);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {  // A_gj and P_gj, j = 2t + e
+            for (int e = 1; e >= 0; --e) {
                 const int j = 2 * t + e;
-                float dec = nk[j];
-#pragma unroll
-                for (int l = 1; l < kTok; ++l)
-                    if (l > j && l <= g) dec *= al[l];
-                if (j < g) sA[g][j] = be[g] * nk[g] * dec * ck[e];
-                if (j <= g) sP[g][j] = nq[g] * dec * ck[2 + e];
+                const float f = my.nk[j] * dec;
+                my.A[g][j] = be[g] * nkg * f * ck[e];
+                my.P[g][j] = nqg * f * ck[2 + e];
+                if (e && j <= g) dec *= al[j];
             }
-            if (lane < kTok) {
-                float x = 1.f, y = 1.f;
-#pragma unroll
-                for (int l = 0; l < kTok; ++l) {
-                    if (l <= lane) x *= al[l];
-                    else y *= al[l];  // 1 behind the last token
-                }
-                ga[lane] = x * nk[lane];
-                gb[lane] = x * nq[lane];
-                cf[lane] = y * nk[lane];
-                if (lane == kTok - 1) gall = x;
+            // the decays up to token g (t = 0), behind it (t = 1), all (t = 2)
+            const float run_of = decay_between(dk, t == 1 ? g + 1 : 0, t == 0 ? g + 1 : kTok);
+            if (t == 0) {
+                my.ga[g] = run_of * nkg;
+                my.gb[g] = run_of * nqg;
+            } else if (t == 1) {
+                my.cf[g] = run_of * nkg;
             }
+            if (lane == 2) gall = run_of;
             __syncwarp();
-            // column j of T = (I + A)^-1 diag(beta), then of M = P T
-            const int j = lane % kTok;
-            float x[kTok];
-#pragma unroll
-            for (int i = 0; i < kTok; ++i) {
-                x[i] = i == j ? 1.f : 0.f;
-#pragma unroll
-                for (int l = 0; l < i; ++l)
-                    if (l >= j) x[i] -= sA[i][l] * x[l];
-            }
-            const float b = be[j];
-            for (int i = g / 2; i < kTok; i += 4) {
-                float p = 0.f, xi = 0.f;
-#pragma unroll
-                for (int l = 0; l < kTok; ++l)
-                    if (l >= j && l <= i) {
-                        p += sP[i][l] * x[l];
-                        if (l == i) xi = x[l];
-                    }
-                if (j <= i) {
-                    tm[0][i][j] = b * xi;
-                    tm[1][i][j] = b * p;
-                }
-            }
+            solve_tokens(my.A, my.P, be, m, lane, my.tm);
         }
         // the rows' products with k and q, the state's three parts apart
-        float ak[3][4] = {}, aq[3][4] = {};
+        float ak[2][4] = {}, aq[2][4] = {};
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
             uint32_t b[4], p[4][3];
@@ -228,8 +210,8 @@ decode_chunks_tc_kernel(RunsArgs a, int row_blocks) {
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
                 const uint32_t left[4] = {p[0][i], p[1][i], p[2][i], p[3][i]};
-                mma16(ak[i], left, b[0], b[1]);
-                mma16(aq[i], left, b[2], b[3]);
+                mma16(ak[i > 0], left, b[0], b[1]);
+                mma16(aq[i > 0], left, b[2], b[3]);
             }
         }
         __syncthreads();  // T and M are there
@@ -237,7 +219,7 @@ decode_chunks_tc_kernel(RunsArgs a, int row_blocks) {
         float r[4], all[2][kTok];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            r[i] = v[i] - ga[2 * t + i % 2] * (ak[0][i] + (ak[1][i] + ak[2][i]));
+            r[i] = v[i] - my.ga[2 * t + i % 2] * (ak[0][i] + ak[1][i]);
 #pragma unroll
         for (int j = 0; j < kTok; ++j) {
             all[0][j] = __shfl_sync(0xffffffffu, r[j % 2], lane / 4 * 4 + j / 2);
@@ -251,21 +233,21 @@ decode_chunks_tc_kernel(RunsArgs a, int row_blocks) {
             float T[kTok], M[kTok];
 #pragma unroll
             for (int j = 0; j < kTok; j += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(&tm[0][i][j]);
-                const float4 y = *reinterpret_cast<const float4 *>(&tm[1][i][j]);
+                const float4 x = *reinterpret_cast<const float4 *>(&my.tm[0][i][j]);
+                const float4 y = *reinterpret_cast<const float4 *>(&my.tm[1][i][j]);
                 T[j] = x.x; T[j + 1] = x.y; T[j + 2] = x.z; T[j + 3] = x.w;
                 M[j] = y.x; M[j + 1] = y.y; M[j + 2] = y.z; M[j + 3] = y.w;
             }
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                float uu = 0.f, out = gb[i] * (aq[0][2 * w + e] + (aq[1][2 * w + e] + aq[2][2 * w + e]));
+                float uu = 0.f, out = my.gb[i] * (aq[0][2 * w + e] + aq[1][2 * w + e]);
 #pragma unroll
                 for (int j = 0; j < kTok; ++j)
                     if (j <= i) {  // what a later token holds stays out
                         uu += T[j] * all[w][j];
                         out += M[j] * all[w][j];
                     }
-                u[2 * w + e] = i < m ? cf[i] * uu : 0.f;
+                u[2 * w + e] = i < m ? my.cf[i] * uu : 0.f;
                 if (op && i < m && (w ? in1 : in0))
                     op[(long long)(c0 + i) * a.Hv * a.Dv + (w ? r1 : r0)] = from_f32<__nv_bfloat16>(out);
             }
