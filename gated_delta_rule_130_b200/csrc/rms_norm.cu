@@ -291,52 +291,28 @@ rms_fwd_any(NormArgs a) {
 // Backward, a row in registers; each block takes the rows blockIdx.x * RPB + ... in
 // steps of the grid, the next row's loads being issued before this row's sums, keeps
 // its columns' sums for dw in registers and leaves them in partial[blockIdx.x].
-// The grid is the blocks that fit at once, 148 times this many (more than one round of
-// blocks leaves SMs idle in the last: 128 threads of 152 registers, 3 per SM with a
-// grid of 592, took 92.7 us on 16384 x 2048; 4 per SM of 128 registers 62.1 us).
+// The grid is the blocks that fit at once, 148 times this many: more than one round of
+// blocks leaves SMs idle in the last.  On 16384 x 2048 bf16 with d_res: 128 threads to a
+// row with the next row in registers, 3 blocks per SM of 152 registers and a grid of 592
+// took 92.7 us, 4 of 128 registers 62.8 us, the ring with 5 blocks 55.1 us.
 template <int TPR, int IT> constexpr int kBwdPerSM =
-    TPR > 256 ? 1 : TPR == 256 ? 2 : TPR == 128 ? (IT == 1 ? 6 : 4) : IT == 1 ? 3 : 2;
+    TPR > 256 ? 1 : TPR == 256 ? 2 : TPR == 128 ? 5 : IT == 1 ? 3 : 2;
 constexpr int kMostBwdBlocks = 148 * 6;
 
-template <typename T, int VEC, int IT> struct RowRaw {
-    Raw<T, VEC> x[IT], dy[IT], g[IT], dr[IT];
-};
-template <typename T, int VEC, int TPR, int IT>
-__device__ __forceinline__ void load_row(const NormArgs &a, int r, int sub, RowRaw<T, VEC, IT> &v) {
-    const Row at(a, r);
-    const T *x = at.of<T>(a.x, a.x_stride), *dy = at.of<T>(a.dy, a.dy_stride);
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int c = (i * TPR + sub) * VEC;
-        if (c < a.D) {
-            v.x[i] = load_raw<T, VEC>(x + c);
-            v.dy[i] = load_raw<T, VEC>(dy + c);
-        }
-    }
-    if (a.gate) {
-        const T *gate = at.of<T>(a.gate, a.gate_stride);
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int c = (i * TPR + sub) * VEC;
-            if (c < a.D) v.g[i] = load_raw<T, VEC>(gate + c);
-        }
-    }
-    if (a.d_res) {
-        const T *dres = at.of<T>(a.d_res, a.dres_stride);
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int c = (i * TPR + sub) * VEC;
-            if (c < a.D) v.dr[i] = load_raw<T, VEC>(dres + c);
-        }
-    }
-}
-
-template <typename T, int VEC, int TPR, int IT>
+// A row's vectors of x, dy, d_res and gate: in registers (the next row's beside this
+// row's) or, 128 threads to a row, in a ring of shared memory that the rows come into
+// asynchronously, S - 1 ahead, each thread's own part by itself.
+template <typename T, int VEC, int TPR, int IT, bool GATE>
 __global__ void __launch_bounds__(TPR > 32 ? TPR : 256, kBwdPerSM<TPR, IT>)
 rms_bwd(NormArgs a) {
     constexpr int RPB = TPR > 32 ? 1 : 256 / TPR;
+    constexpr bool RING = TPR == 128;
+    constexpr int S = 2, NT = GATE ? 4 : 3;
     __shared__ float part[2][32][2];
     __shared__ float cols[TPR > 32 ? 1 : VEC * TPR * IT];
+    __shared__ __align__(16) Raw<T, VEC> ring[RING ? S : 1][RING ? NT : 1][RING ? IT : 1]
+                                             [RING ? TPR : 1];
+    Raw<T, VEC> held[RING ? 1 : 2][RING ? 1 : NT][RING ? 1 : IT];
     const int sub = threadIdx.x % TPR;
     float dw[IT][VEC];
 #pragma unroll
@@ -344,12 +320,54 @@ rms_bwd(NormArgs a) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) dw[i][e] = 0.f;
     const int step = gridDim.x * RPB;
-    int r = blockIdx.x * RPB + threadIdx.x / TPR, turn = 0;
-    RowRaw<T, VEC, IT> cur, next;
-    if (r < a.rows) load_row<T, VEC, TPR, IT>(a, r, sub, cur);
+    int r = blockIdx.x * RPB + threadIdx.x / TPR, turn = 0, slot = 0;
+    // row r into slot `to` of the ring (or the second of the registers)
+    const auto fetch = [&](int row, int to) {
+        if (row < a.rows) {
+            const Row at(a, row);
+            const T *p[4] = {at.of<T>(a.x, a.x_stride), at.of<T>(a.dy, a.dy_stride),
+                             a.d_res ? at.of<T>(a.d_res, a.dres_stride) : nullptr,
+                             GATE ? at.of<T>(a.gate, a.gate_stride) : nullptr};
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                if (p[n])
+#pragma unroll
+                    for (int i = 0; i < IT; ++i) {
+                        const int c = (i * TPR + sub) * VEC;
+                        if (c < a.D) {
+                            if constexpr (RING) copy_async<T, VEC>(&ring[to][n][i][sub], p[n] + c);
+                            else held[1][n][i] = load_raw<T, VEC>(p[n] + c);
+                        }
+                    }
+        }
+        if constexpr (RING) copy_commit();
+    };
+    const auto in = [&](int n, int i) {
+        if constexpr (RING) return ring[slot][n][i][sub];
+        else return held[0][n][i];
+    };
+    const auto advance = [&] {
+        if constexpr (!RING)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < IT; ++i) held[0][n][i] = held[1][n][i];
+    };
+    if constexpr (RING) {
+#pragma unroll
+        for (int k = 0; k < S - 1; ++k) fetch(r < a.rows - k * step ? r + k * step : a.rows, k);
+    } else {
+        fetch(r, 0);
+        advance();
+    }
     for (int r0 = blockIdx.x * RPB; r0 < a.rows; r0 += step, r += step, turn ^= 1) {
         const int width = r < a.rows ? a.D : 0;
-        if (r < a.rows - step) load_row<T, VEC, TPR, IT>(a, r + step, sub, next);
+        if constexpr (RING) {
+            copy_wait<S - 2>();  // this row has come
+            fetch(r < a.rows - (S - 1) * step ? r + (S - 1) * step : a.rows, slot ? slot - 1 : S - 1);
+        } else {
+            fetch(r < a.rows - step ? r + step : a.rows, 1);
+        }
         const long long out = (long long)r * a.D;
         float h[IT][VEC], t[IT][VEC];  // t: w dn
         float p[VEC] = {}, q[VEC] = {}, ss = 0.f, sd = 0.f;
@@ -358,12 +376,12 @@ rms_bwd(NormArgs a) {
             const int c = (i * TPR + sub) * VEC;
             if (c < width) {
                 float w[VEC];
-                widen(cur.x[i], h[i]);
-                widen(cur.dy[i], t[i]);
+                widen(in(0, i), h[i]);
+                widen(in(1, i), t[i]);
                 load_param<T, VEC>(a.weight, c, a.weight_f32, w);
-                if (a.gate) {
+                if constexpr (GATE) {
                     float g[VEC], sig[VEC];
-                    widen(cur.g[i], g);
+                    widen(in(3, i), g);
                     fast_sigmoid<VEC>(g, sig);
                     mul_vec<VEC>(g, sig);
                     mul_vec<VEC>(t[i], g);
@@ -400,10 +418,10 @@ rms_bwd(NormArgs a) {
             const int c = (i * TPR + sub) * VEC;
             if (c < width) {
                 float dx[VEC], dn[VEC];
-                widen(cur.dy[i], dn);
-                if (a.gate) {
+                widen(in(1, i), dn);
+                if constexpr (GATE) {
                     float g[VEC], w[VEC], dg[VEC];
-                    widen(cur.g[i], g);
+                    widen(in(3, i), g);
                     load_param<T, VEC>(a.weight, c, a.weight_f32, w);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
@@ -414,7 +432,7 @@ rms_bwd(NormArgs a) {
                     store_vec(static_cast<T *>(a.dgate) + out + c, dg);
                 }
                 if (a.d_res) {
-                    widen(cur.dr[i], dx);
+                    widen(in(2, i), dx);
                 } else {
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) dx[e] = 0.f;
@@ -432,7 +450,8 @@ rms_bwd(NormArgs a) {
                 store_vec(static_cast<T *>(a.dx) + out + c, dx);
             }
         }
-        cur = next;
+        advance();
+        slot = slot + 1 == S ? 0 : slot + 1;
     }
     float *mine = a.partial + (long long)blockIdx.x * a.D;
     if (TPR > 32) {
@@ -547,7 +566,8 @@ void run_bwd(const NormArgs &a, cudaStream_t st) {
     constexpr int rpb = TPR > 32 ? 1 : 256 / TPR, threads = TPR > 32 ? TPR : 256;
     const int need = (a.rows + rpb - 1) / rpb, most = 148 * kBwdPerSM<TPR, IT>;
     const int blocks = need < most ? need : most;
-    rms_bwd<T, VEC, TPR, IT><<<blocks, threads, 0, st>>>(a);
+    if (a.gate) rms_bwd<T, VEC, TPR, IT, true><<<blocks, threads, 0, st>>>(a);
+    else rms_bwd<T, VEC, TPR, IT, false><<<blocks, threads, 0, st>>>(a);
     rms_bwd_sum<<<(a.D + 31) / 32, 1024, 0, st>>>(a.partial, a.dw, blocks, a.D);
 }
 
