@@ -4,12 +4,14 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "../../include/gdn.h"
 #include "kernels.h"
 
 namespace {
 
-constexpr int kMaxSeqs = 65535, kMaxHeads = 65535, kMaxNormD = 1 << 20, kMaxChannels = 1 << 24;
+constexpr int kMaxSeqs = 65535, kMaxTokens = 1 << 30, kMaxHeads = 65535, kMaxNormD = 1 << 20, kMaxChannels = 1 << 24;
 // (rows - 1) * stride + width, in bytes, stays inside size_t for 2^31 rows
 constexpr long long kMaxStride = 1ll << 30, kMaxBlocks = 0x7fffffffll, kMaxPool = 1ll << 40;
 
@@ -36,7 +38,7 @@ gdn_status_t status(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_
 // Offsets and slots of a packed batch.
 gdn_status_t check_seqs(const int *slots, const int *cu, int N, int total) {
     if (N < 0 || total < 0) return GDN_ERR_INVALID_ARG;
-    if (N > kMaxSeqs) return GDN_ERR_UNSUPPORTED;
+    if (N > kMaxSeqs || total > kMaxTokens) return GDN_ERR_UNSUPPORTED;
     if (!cu && N != total) return GDN_ERR_INVALID_ARG;
     if ((slots && !aligned(slots, 16)) || (cu && !aligned(cu, 16))) return GDN_ERR_INVALID_ARG;
     return GDN_OK;
@@ -72,7 +74,7 @@ gdn_status_t check_norm(int tokens, int heads, int D, float eps, gdn_dtype_t dty
     if (tokens < 0 || heads < 0 || D <= 0 || !dtype_ok(dtype)) return GDN_ERR_INVALID_ARG;
     if (param_dtype != GDN_F32 && param_dtype != dtype) return GDN_ERR_INVALID_ARG;
     if (!(eps >= 0.f) || isinf(eps)) return GDN_ERR_INVALID_ARG;
-    if (D > kMaxNormD || (long long)tokens * heads > kMaxBlocks) return GDN_ERR_UNSUPPORTED;
+    if (D > kMaxNormD || (long long)tokens * heads > kMaxTokens) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 
@@ -188,7 +190,7 @@ gdn_status_t gdn_short_conv_fwd(const void *x, const void *weight, const void *b
 }
 
 size_t gdn_short_conv_bwd_workspace_size(int total, int C, int W) {
-    if (total <= 0 || C <= 0 || C > kMaxChannels || W < 2 || W > 4) return 0;
+    if (total <= 0 || total > kMaxTokens || C <= 0 || C > kMaxChannels || W < 2 || W > 4) return 0;
     return gdn::short_conv_bwd_bytes(total, C, W);
 }
 

@@ -366,7 +366,7 @@ gdn_status_t gdn_decode_step_cw(const void *q, const void *k, const void *v,
  *                not written (a draft's outputs before it is accepted; several
  *                sequences may then share a slot).
  * Limits: those of gdn_decode_step, Hv a multiple of Hk, N <= 65535,
- * N * Hv * Dv < 2^31, n_slots * Hv <= 2^40.  o and states overlap nothing else.
+ * total <= 2^30, N * Hv * Dv < 2^31, n_slots * Hv <= 2^40.  o and states overlap nothing else.
  */
 #define GDN_FLAG_READ_ONLY 4u
 gdn_status_t gdn_decode_runs(const void *q, const void *k, const void *v,
@@ -392,7 +392,7 @@ gdn_status_t gdn_decode_runs(const void *q, const void *k, const void *v,
  *   slots, cu_seqlens : as for gdn_decode_runs.
  *   silu    : nonzero: y = silu(z).
  * No y may overlap another argument (column slices of one array are apart).  Limits:
- * N <= 65535, C <= 2^24, ceil(C / 128) * total < 2^31.
+ * N <= 65535, total <= 2^30, C <= 2^24, ceil(C / 128) * total < 2^31.
  */
 gdn_status_t gdn_short_conv_fwd(const void *x, const void *weight, const void *bias, void *states,
                                 const int *slots, const int *cu_seqlens, void *const *y,
@@ -431,7 +431,7 @@ size_t gdn_short_conv_bwd_workspace_size(int total, int C, int W);
  *             scale = max|y| / 448 of the group, float32 [rows, D / quant_group]
  *             (groups whose largest magnitude is below 1e-30: 1e-30 / 448).  A NaN
  *             or an infinity in a group of y makes its scale and values NaN.
- * Limits: 1 <= D <= 2^20, tokens * heads < 2^31.
+ * Limits: 1 <= D <= 2^20, tokens * heads <= 2^30.
  */
 gdn_status_t gdn_rms_norm_fwd(const void *x, const void *weight, const void *residual,
                               const void *gate, void *y, float *scale, void *h_out, int tokens,

@@ -100,29 +100,36 @@ def test_raw_inputs(gdn, dtype):
     check(gdn, d, offsets(lens), [2, 0, 1], dtype, l2norm_qk=True, gate_logits=True)
 
 
-def test_padding_rows_and_rows_behind(gdn):
+# the kernels: runs of several tokens in float32 (at a vector and an odd width) and in bf16
+# on the tensor cores, and batches of single tokens (token by token)
+KERNELS = [(F32, 32, 24, [3, 2, 1, 9]), (F32, 37, 24, [3, 2, 1, 9]), (BF16, 128, 40, [3, 2, 1, 9]),
+           (BF16, 64, 136, [8, 2, 1, 17]), (F32, 128, 24, [1, 1, 1, 1]), (BF16, 72, 24, [2, 1, 1, 1])]
+
+
+@pytest.mark.parametrize("dtype,Dk,Dv,lens", KERNELS)
+def test_padding_rows_and_rows_behind(gdn, dtype, Dk, Dv, lens):
     # rows of padding (a slot below 0 or behind the pool), rows behind the last sequence and
     # unused slots may hold anything and stay out of the results
-    lens = [3, 2, 1, 9]
-    d = draw(sum(lens), 1, 2, 32, 24, 6, F32, 11, behind=4)
+    d = draw(sum(lens), 1, 2, Dk, Dv, 6, dtype, 11, behind=4)
     cu = offsets(lens)
     for n in ("q", "k", "v", "la", "be"):
         d[n][cu[1]:cu[3]] = float("nan")
         d[n][cu[4]:] = float("inf")
     d["states"][4] = float("nan")
-    o, S = check(gdn, d, cu, [5, -1, 6, 2], F32)
+    o, S = check(gdn, d, cu, [5, -1, 6, 2], dtype)
     assert (o[cu[1]:cu[3]] == 0).all() and (o[cu[4]:] == 7).all()
     assert S[4].isnan().all() and torch.equal(S[0], d["states"][0])
 
 
-def test_a_slot_named_twice(gdn):
+@pytest.mark.parametrize("dtype,Dk,Dv,lens", [(F32, 48, 40, [0, 2, 3, 2, 9]), (BF16, 128, 40, [0, 2, 3, 2, 9]),
+                                              (BF16, 48, 40, [0, 1, 2, 1, 1])])
+def test_a_slot_named_twice(gdn, dtype, Dk, Dv, lens):
     # the first sequence with tokens has it; read-only runs share it
-    lens = [0, 2, 3, 2, 1]
-    d = draw(sum(lens), 1, 2, 48, 40, 4, F32, 12)
-    o, _ = check(gdn, d, offsets(lens), [1, 3, 1, 1, 3], F32)
-    assert (o[5:] == 0).all()
-    o, _ = check(gdn, d, offsets(lens), [1, 3, 1, 1, 3], F32, update=False)
-    assert (o[5:] != 0).any()
+    d = draw(sum(lens), 1, 2, Dk, Dv, 4, dtype, 12)
+    o, _ = check(gdn, d, offsets(lens), [1, 3, 1, 1, 3], dtype)
+    assert (o[sum(lens[:3]):] == 0).all()
+    o, _ = check(gdn, d, offsets(lens), [1, 3, 1, 1, 3], dtype, update=False)
+    assert (o[sum(lens[:3]):] != 0).any()
 
 
 def test_many_sequences_one_slot_twice(gdn):
@@ -134,14 +141,55 @@ def test_many_sequences_one_slot_twice(gdn):
     check(gdn, d, None, slots, F32)
 
 
-def test_gates_at_their_ends(gdn):
+@pytest.mark.parametrize("dtype,Dk", [(F32, 64), (BF16, 64), (BF16, 128), (BF16, 40)])
+def test_gates_at_their_ends(gdn, dtype, Dk):
     # a decay of exactly 0 (log alpha = -inf) in a run, none at all, writes of 0 and 1
     lens = [9, 4]
-    d = draw(sum(lens), 1, 2, 64, 32, 2, F32, 14)
+    d = draw(sum(lens), 1, 2, Dk, 32, 2, dtype, 14)
     d["la"][2] = d["la"][7] = float("-inf")
     d["la"][5], d["la"][10] = 0.0, -1e30
     d["be"][3], d["be"][4] = 0.0, 1.0
-    check(gdn, d, offsets(lens), None, F32)
+    check(gdn, d, offsets(lens), None, dtype)
+
+
+@pytest.mark.parametrize("dtype,Dk", [(F32, 64), (BF16, 128), (F32, 30), (BF16, 64)])
+def test_a_later_token_leaves_the_earlier_ones_alone(gdn, dtype, Dk):
+    # NaN in the fourth token's k and the sixth's v: the outputs before them are what they
+    # were, bit for bit, those behind are NaN
+    d = draw(16, 1, 1, Dk, 32, 2, dtype, 21)
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    run = lambda: gdn.decode_runs(d["q"], d["k"], d["v"], d["la"], d["be"], d["states"].clone(),
+                                  cu_seqlens=dev([0, 8, 16]))
+    a = run()
+    d["k"][3] = float("nan")
+    d["v"][8 + 5] = float("nan")
+    b = run()
+    assert torch.equal(a[:3], b[:3]) and b[3:8].isnan().all()
+    assert torch.equal(a[8:13], b[8:13]) and b[13:].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_equal_keys_without_decay(gdn, dtype):
+    # the same unit key eight times, written with strength 1: each write replaces the last,
+    # and the system that joins the tokens is as far from the identity as it gets
+    d = draw(8, 1, 1, 128, 64, 1, dtype, 22)
+    d["k"][:] = 0.0
+    d["k"][:, :, :16] = 0.25  # |k| = 1, exact in bf16
+    d["la"].zero_()
+    d["be"].fill_(1.0)
+    _, S = check(gdn, d, [0, 8], None, dtype)
+    # S k is the last v
+    got = (S[0, 0].double() @ d["k"][7, 0].double()).cpu()
+    assert (got - d["v"][7, 0].double().cpu()).abs().max() <= 64 * R.U32 * (8 * d["v"].abs().max() + 4).item()
+
+
+@pytest.mark.parametrize("dtype,Dk,Dv", [(BF16, 128, 128), (BF16, 64, 96), (F32, 128, 64), (F32, 256, 20)])
+def test_states_of_all_magnitudes(gdn, dtype, Dk, Dv):
+    # rows of the state from 1e-18 to 1e18: nothing is lost beside larger numbers
+    d = draw(12, 1, 1, Dk, Dv, 2, dtype, 23)
+    d["states"] *= 10.0 ** torch.linspace(-18, 18, Dv, device="cuda")[:, None]
+    d["v"] *= 0
+    check(gdn, d, [0, 4, 12], None, dtype)
 
 
 def test_read_only_then_commit(gdn):
