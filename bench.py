@@ -758,6 +758,63 @@ def run_decode_only(args):
                       "steps": steps}), flush=True)
 
 
+def run_layer_only(args):
+    """--layer-only: the operators around the rule alone, at the headline's layer (16 heads
+    of 128, 16384 tokens) and the decode batch of 256; prints one short JSON line."""
+    torch.cuda.set_device(0)
+    device = torch.device("cuda", 0)
+    from gated_delta_rule_130_b200 import binding as G
+    pk, pk_kind = peaks()
+    T, B, H, D = 16384, 256, 16, 128
+    M = H * D
+    gen = torch.Generator(device=device).manual_seed(3001)
+    rnd = lambda *s: torch.randn(s, generator=gen, device=device).bfloat16()
+    f32 = lambda *s: torch.randn(s, generator=gen, device=device)
+    lens = I.varlen_lengths(12, T, 2002)
+    cu = torch.tensor([0] + lens, device=device).cumsum(0).to(torch.int32)
+    slots = torch.randperm(B, generator=torch.Generator().manual_seed(1)).to(torch.int32).to(device)
+    x, res, dy, wn, wo = rnd(T, M), rnd(T, M), rnd(T, M), rnd(M), rnd(D)
+    z, wc, dz = rnd(T, 3 * M), rnd(3 * M, 4), tuple(rnd(T, M) for _ in range(3))
+    o, gate = rnd(T, H, D), rnd(T, H, D)
+    qkv, la, be = rnd(B, 3, H, D), f32(B, H), f32(B, H)
+    run = rnd(8 * 64, 3, H, D)
+    run_cu = torch.arange(0, 8 * 64 + 1, 8, device=device, dtype=torch.int32)
+    run_la, run_be = f32(8 * 64, H), f32(8 * 64, H)
+    S, Sc = 0.02 * f32(B, H, D, D), rnd(B, 3, 3 * M)
+    state = 4 * H * D * D
+    legs = [  # name, call, bytes that it cannot do without
+        ("rms_norm_fwd 16384 x 2048, residual, e4m3 out",
+         lambda: G.rms_norm_fwd(x, wn, residual=res, quant="row"), T * M * 7),
+        ("rms_norm_bwd 16384 x 2048, residual",
+         lambda: G.rms_norm_bwd(dy, x, wn, d_res=res), T * M * 8),
+        ("rms_norm_fwd gated 16384 x 16 x 128", lambda: G.rms_norm_fwd(o, wo, gate=gate), T * M * 6),
+        ("rms_norm_bwd gated 16384 x 16 x 128",
+         lambda: G.rms_norm_bwd(dy.view(T, H, D), o, wo, gate=gate), T * M * 10),
+        ("short_conv_fwd 16384 x 6144, 12 sequences",
+         lambda: G.short_conv_fwd(z, wc, cu_seqlens=cu, splits=[M] * 3), T * M * 12),
+        ("short_conv_bwd 16384 x 6144, 12 sequences",
+         lambda: G.short_conv_bwd(dz, z, wc, cu_seqlens=cu), T * M * 18),
+        ("short_conv_fwd 256 x 6144, one token of 256 sequences",
+         lambda: G.short_conv_fwd(z[:B], wc, states=Sc, slots=slots, splits=[M] * 3), B * M * (12 + 36)),
+        ("decode_runs one token of 256 sequences",
+         lambda: G.decode_runs(qkv[:, 0], qkv[:, 1], qkv[:, 2], la, be, S, slots=slots, l2norm_qk=True,
+                               gate_logits=True), B * (2 * state + 8 * M + 8 * H)),
+        ("decode_runs 8 tokens of 64 sequences",
+         lambda: G.decode_runs(run[:, 0], run[:, 1], run[:, 2], run_la, run_be, S, slots=slots[:64],
+                               cu_seqlens=run_cu, l2norm_qk=True, gate_logits=True),
+         64 * (2 * state + 8 * (8 * M + 8 * H))),
+    ]
+    stream, steps, out = torch.cuda.current_stream(device), args.steps or 100, []
+    for name, call, nbytes in legs:
+        for _ in range(max(args.warmup, 3)):
+            call()
+        us = 1e3 * time_loop(call, steps, stream, 1) / steps
+        out.append({"op": name, "us": us, "achieved": nbytes / us / 1e3, "unit": "GB/s",
+                    "frac": nbytes / us / 1e3 / pk["hbm_gbs"], "bytes": nbytes})
+    print(json.dumps({"leg": "layer", "ops": out, "peak": pk["hbm_gbs"],
+                      "peak_source": f"{pk_kind} hbm_gbs", "steps": steps}), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -775,9 +832,13 @@ def main():
                     help="time the channel-wise-gate forward alone on --workload (one GPU)")
     ap.add_argument("--bwd-only", action="store_true",
                     help="time the chunkwise backward alone on --workload (one GPU)")
+    ap.add_argument("--layer-only", action="store_true",
+                    help="time the operators around the rule alone (one GPU)")
     args = ap.parse_args()
     if args.bwd_only:
         run_bwd_only(args)
+    elif args.layer_only:
+        run_layer_only(args)
     elif args.decode_only:
         run_decode_only(args)
     elif args.cw_only:

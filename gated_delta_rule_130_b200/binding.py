@@ -532,10 +532,12 @@ def _call(dev: int, f, *args):
 
 
 def _scratch(need: int, workspace, like, dev: int):
-    if workspace is None:
-        return like.new_empty(max(need, 16), dtype=torch.uint8).data_ptr(), max(need, 16)
-    return (_dense(workspace, "workspace", workspace.dtype, dev),
-            workspace.numel() * workspace.element_size())
+    """Pointer and bytes of the workspace, a new one where none or too small a one is given."""
+    if workspace is not None:
+        nbytes = workspace.numel() * workspace.element_size()
+        if nbytes >= need:
+            return _dense(workspace, "workspace", workspace.dtype, dev), nbytes
+    return like.new_empty(max(need, 16), dtype=torch.uint8).data_ptr(), max(need, 16)
 
 
 def _sequences(cu_seqlens, slots, total, dev: int):
