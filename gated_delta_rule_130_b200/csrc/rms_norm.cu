@@ -307,6 +307,7 @@ __global__ void __launch_bounds__(TPR > 32 ? TPR : 256, kBwdPerSM<TPR, IT>)
 rms_bwd(NormArgs a) {
     constexpr int RPB = TPR > 32 ? 1 : 256 / TPR;
     constexpr bool RING = TPR == 128;
+    constexpr bool KEEP = GATE && IT == 1;  // what the gate gives is kept, not formed again
     constexpr int S = 2, NT = GATE ? 4 : 3;
     __shared__ float part[2][32][2];
     __shared__ float cols[TPR > 32 ? 1 : VEC * TPR * IT];
@@ -370,6 +371,7 @@ rms_bwd(NormArgs a) {
         }
         const long long out = (long long)r * a.D;
         float h[IT][VEC], t[IT][VEC];  // t: w dn
+        float dg[1][VEC], dn[1][VEC];
         float p[VEC] = {}, q[VEC] = {}, ss = 0.f, sd = 0.f;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
@@ -383,8 +385,19 @@ rms_bwd(NormArgs a) {
                     float g[VEC], sig[VEC];
                     widen(in(3, i), g);
                     fast_sigmoid<VEC>(g, sig);
+                    if constexpr (KEEP) {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) {
+                            // dy w silu'(g), which waits for rstd
+                            dg[0][e] = t[i][e] * w[e] * sig[e] * (1.f + g[e] * (1.f - sig[e]));
+                        }
+                    }
                     mul_vec<VEC>(g, sig);
                     mul_vec<VEC>(t[i], g);
+                    if constexpr (KEEP) {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) dn[0][e] = t[i][e];
+                    }
                 }
                 mul_vec<VEC>(t[i], w);
                 fma_vec<VEC>(h[i], h[i], p);
@@ -417,19 +430,29 @@ rms_bwd(NormArgs a) {
         for (int i = 0; i < IT; ++i) {
             const int c = (i * TPR + sub) * VEC;
             if (c < width) {
-                float dx[VEC], dn[VEC];
-                widen(in(1, i), dn);
-                if constexpr (GATE) {
-                    float g[VEC], w[VEC], dg[VEC];
-                    widen(in(3, i), g);
-                    load_param<T, VEC>(a.weight, c, a.weight_f32, w);
+                float dx[VEC], d[VEC];
+                if constexpr (KEEP) {
+                    float out_g[VEC];
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        const float sig = fast_sigmoid(g[e]);
-                        dg[e] = dn[e] * (h[i][e] * rstd) * w[e] * sig * (1.f + g[e] * (1.f - sig));
-                        dn[e] *= g[e] * sig;
+                        out_g[e] = dg[0][e] * (h[i][e] * rstd);
+                        d[e] = dn[0][e];
                     }
-                    store_vec(static_cast<T *>(a.dgate) + out + c, dg);
+                    store_vec(static_cast<T *>(a.dgate) + out + c, out_g);
+                } else {
+                    widen(in(1, i), d);
+                }
+                if constexpr (GATE && !KEEP) {
+                    float g[VEC], w[VEC], sig[VEC], out_g[VEC];
+                    widen(in(3, i), g);
+                    load_param<T, VEC>(a.weight, c, a.weight_f32, w);
+                    fast_sigmoid<VEC>(g, sig);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        out_g[e] = d[e] * (h[i][e] * rstd) * w[e] * sig[e] * (1.f + g[e] * (1.f - sig[e]));
+                        d[e] *= g[e] * sig[e];
+                    }
+                    store_vec(static_cast<T *>(a.dgate) + out + c, out_g);
                 }
                 if (a.d_res) {
                     widen(in(2, i), dx);
@@ -446,7 +469,7 @@ rms_bwd(NormArgs a) {
                 fma_vec<VEC>(h[i], backs, dx);
                 fma_vec<VEC>(t[i], rstds, dx);
                 fma_vec<VEC>(h[i], rstds, n);
-                fma_vec<VEC>(dn, n, dw[i]);
+                fma_vec<VEC>(d, n, dw[i]);
                 store_vec(static_cast<T *>(a.dx) + out + c, dx);
             }
         }
