@@ -594,9 +594,13 @@ void run_bwd(const NormArgs &a, cudaStream_t st) {
     rms_bwd_sum<<<(a.D + 31) / 32, 1024, 0, st>>>(a.partial, a.dw, blocks, a.D);
 }
 
-// From this many rows on a warp takes a row of up to 256 vectors by itself; fewer rows
-// are shared by a block each, so that they still reach more SMs.
-constexpr int kManyRows = 148 * 8;
+// Threads and vectors per row, from sweeps on bf16 rows (us; plain / with residual and
+// e4m3): 16384 rows of 2048: 64 threads of 4 vectors 24.9 / 38.2, 128 of 2 26.7 / 40.2,
+// 256 of 1 35.6 / 50.7, a warp of 8 44.5 / 41.0; 1184 rows: 3.7 / 4.1 and 3.1 / 4.2 for
+// the first two, which meet near 4736 rows.  16384 rows of 1024: 64 of 2 12.7 / 20.7,
+// 32 of 4 13.3 / 21.8, 128 of 1 16.4 / 25.3; of 8192: 256 of 4 106.6 / 152.5, 512 of 2
+// 141.0 / 188.6.
+constexpr int kManyRows = 148 * 32;
 
 template <typename T, int VEC>
 cudaError_t fwd_t(const NormArgs &a, cudaStream_t st) {
@@ -613,18 +617,20 @@ cudaError_t fwd_t(const NormArgs &a, cudaStream_t st) {
         run_fwd<T, VEC, 16, 2>(a, st);
     } else if (nv <= 64) {
         run_fwd<T, VEC, 32, 2>(a, st);
-    } else if (nv <= 128 && a.rows >= kManyRows) {
-        run_fwd<T, VEC, 32, 4>(a, st);
+    } else if (nv <= 128) {
+        run_fwd<T, VEC, 64, 2>(a, st);
     } else if (nv <= 256 && a.rows >= kManyRows) {
-        run_fwd<T, VEC, 32, 8>(a, st);
+        run_fwd<T, VEC, 64, 4>(a, st);
     } else if (nv <= 256) {
         run_fwd<T, VEC, 128, 2>(a, st);
+    } else if (nv <= 512 && a.rows >= kManyRows) {
+        run_fwd<T, VEC, 128, 4>(a, st);
     } else if (nv <= 512) {
         run_fwd<T, VEC, 256, 2>(a, st);
     } else if (nv <= 1024) {
-        run_fwd<T, VEC, 512, 2>(a, st);
+        run_fwd<T, VEC, 256, 4>(a, st);
     } else if (nv <= 2048) {
-        run_fwd<T, VEC, 1024, 2>(a, st);
+        run_fwd<T, VEC, 512, 4>(a, st);
     } else {
         run_fwd<T, VEC, 1024, 4>(a, st);
     }

@@ -15,15 +15,6 @@ __device__ __forceinline__ float2 decay_pair(float la, float be, unsigned flags)
     return make_float2(expf(la), be);
 }
 
-// Whether an earlier sequence with tokens names this slot (seen by every lane that
-// calls with its own share of the sequences).
-__device__ __forceinline__ int slot_taken(const RunsArgs &a, int n, int slot, int from, int step) {
-    int taken = 0;
-    for (int i = from; i < n; i += step)
-        if (a.slots[i] == slot) taken |= !a.cu || a.cu[i] < a.cu[i + 1];
-    return taken;
-}
-
 // x of row p, eight floats 16 bytes aligned.
 __device__ __forceinline__ void load8(const float *p, float (&x)[kRunTokens]) {
 #pragma unroll

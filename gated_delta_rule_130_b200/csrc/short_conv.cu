@@ -193,10 +193,7 @@ conv_fwd(ConvArgs a, unsigned ctiles, int tile) {
                 todo &= todo - 1;
                 const int m = __shfl_sync(0xffffffffu, n, k);
                 const int want = __shfl_sync(0xffffffffu, slot, k);
-                int taken = 0;
-#pragma unroll 4
-                for (int l = lane; l < m; l += 32)
-                    if (a.slots[l] == want) taken |= !a.cu || a.cu[l] < a.cu[l + 1];
+                const int taken = slot_taken(a.slots, a.cu, m, want, lane, 32);
                 if (__any_sync(0xffffffffu, taken) && n == m) f |= kPadding;
             }
         }
@@ -358,11 +355,7 @@ conv_few(ConvArgs a, unsigned ctiles) {
     // of the sequences with tokens that name one slot the first has it
     bool zero = padding;
     if (held && a.slots) {
-        int taken = 0;
-#pragma unroll 4
-        for (int k = lane; k < n; k += 32)
-            if (a.slots[k] == slot) taken |= !a.cu || a.cu[k] < a.cu[k + 1];
-        zero = __any_sync(0xffffffffu, taken);
+        zero = __any_sync(0xffffffffu, slot_taken(a.slots, a.cu, n, slot, lane, 32));
     }
     if (!live) return;
     const int p = part_of(a, cc);
