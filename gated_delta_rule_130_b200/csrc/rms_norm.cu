@@ -10,6 +10,11 @@
 // Both directions read and write each element once and are bound by HBM.  A row is
 // held in the registers of TPR threads (part of a warp, a warp or a block) as IT
 // vectors of 16 bytes each; sums are float32.
+//
+// On B200, bf16: 16384 rows of 2048 with residual to e4m3 39.1 us (235 MB, 0.92 of the
+// measured copy rate); 262144 gated rows of 128 35.6 us (201 MB, 0.86); gradients of
+// 16384 x 2048 with d_res 55 us (268 MB, 0.74, 5 us of it the sum over the blocks), of
+// the gated rows 72 us (336 MB, 0.71).
 #include <cuda_fp8.h>
 
 #include "kernels.h"
@@ -549,19 +554,27 @@ rms_bwd_any(NormArgs a) {
     }
 }
 
-// dw[c] = sum over the blocks' partial sums, always in the same order.
+// dw[c] = sum over the blocks' partial sums, always in the same order: a block takes 8
+// columns (a sector of each row), 128 threads to a column.
+constexpr int kSumCols = 8;
 __global__ void __launch_bounds__(1024)
 rms_bwd_sum(const float *partial, float *dw, int blocks, int D) {
-    __shared__ float part[32][33];
-    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32, c = blockIdx.x * 32 + tx;
+    __shared__ float part[32][kSumCols];
+    const int col = threadIdx.x % kSumCols, c = blockIdx.x * kSumCols + col;
     float s = 0.f;
     if (c < D)
 #pragma unroll 8
-        for (int b = ty; b < blocks; b += 32) s += partial[(long long)b * D + c];
-    part[ty][tx] = s;
+        for (int b = threadIdx.x / kSumCols; b < blocks; b += 1024 / kSumCols)
+            s += partial[(long long)b * D + c];
+    s += __shfl_xor_sync(0xffffffffu, s, 8);
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    if (threadIdx.x % 32 < kSumCols) part[threadIdx.x / 32][col] = s;
     __syncthreads();
-    s = lanes_reduce<32, false>(part[tx][ty]);
-    if (tx == 0 && blockIdx.x * 32 + ty < D) dw[blockIdx.x * 32 + ty] = s;
+    if (threadIdx.x >= kSumCols || c >= D) return;
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) s += part[w][col];
+    dw[c] = s;
 }
 
 // Partial sums a workspace has room for.
@@ -591,7 +604,7 @@ void run_bwd(const NormArgs &a, cudaStream_t st) {
     const int blocks = need < most ? need : most;
     if (a.gate) rms_bwd<T, VEC, TPR, IT, true><<<blocks, threads, 0, st>>>(a);
     else rms_bwd<T, VEC, TPR, IT, false><<<blocks, threads, 0, st>>>(a);
-    rms_bwd_sum<<<(a.D + 31) / 32, 1024, 0, st>>>(a.partial, a.dw, blocks, a.D);
+    rms_bwd_sum<<<(a.D + kSumCols - 1) / kSumCols, 1024, 0, st>>>(a.partial, a.dw, blocks, a.D);
 }
 
 // Threads and vectors per row, from sweeps on bf16 rows (us; plain / with residual and
@@ -643,7 +656,7 @@ cudaError_t bwd_t(const NormArgs &a, cudaStream_t st) {
     if (!vectors_fit(a, sizeof(T)) || nv > 2048) {
         const int blocks = bwd_blocks(a.rows);
         rms_bwd_any<T><<<blocks, kAnyThreads, 0, st>>>(a);
-        rms_bwd_sum<<<(a.D + 31) / 32, 1024, 0, st>>>(a.partial, a.dw, blocks, a.D);
+        rms_bwd_sum<<<(a.D + kSumCols - 1) / kSumCols, 1024, 0, st>>>(a.partial, a.dw, blocks, a.D);
     } else if (nv <= 4) {
         run_bwd<T, VEC, 4, 1>(a, st);
     } else if (nv <= 8) {

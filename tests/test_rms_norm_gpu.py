@@ -144,9 +144,9 @@ def test_slices_and_float32_weights(gdn):
 
 
 def bwd_roundings(D, rows):
-    # two sums over a row and their products; dw: a block's rows in a chain, its row
-    # groups (64 at most) in a chain, then 592 blocks at most, 32 ways
-    return max(32, D / 256) + 64 + rows / 592 + 64 + 24
+    # two sums over a row and their products; dw: a block's rows in a chain (148 blocks at
+    # least), its row groups (64 at most) in a chain, then 888 blocks at most, 128 ways
+    return max(32, D / 256) + 64 + rows / 148 + 64 + 24
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
