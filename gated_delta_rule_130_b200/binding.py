@@ -507,6 +507,8 @@ def _rows(t, name: str, dtype, dev: int):
     if shape[0] > 1 and t.is_contiguous():
         return t.data_ptr(), t.stride(0)
     strides = t.stride()
+    if len(shape) == 3 and shape[0] > 1 and strides[2] == 1 and strides[1] == shape[2]:
+        return t.data_ptr(), strides[0]
     width = 1
     for i in range(len(shape) - 1, 0, -1):
         n = shape[i]
@@ -529,6 +531,18 @@ def _call(dev: int, f, *args):
         return f(*args, torch._C._cuda_getCurrentRawStream(dev))
     with torch.cuda.device(dev):
         return f(*args, torch._C._cuda_getCurrentRawStream(dev))
+
+
+def _like_parts(x, shapes):
+    """New arrays of x's type and device, from one allocation where they are alike and each
+    keeps a 16-byte boundary."""
+    first = shapes[0]
+    n = 1
+    for k in first:
+        n *= k
+    if len(shapes) > 1 and n % 8 == 0 and all(s == first for s in shapes):
+        return x.new_empty((len(shapes), *first)).unbind(0)
+    return tuple([x.new_empty(s) for s in shapes])
 
 
 def _scratch(need: int, workspace, like, dev: int):
@@ -673,7 +687,7 @@ def short_conv_fwd(x, weight, bias=None, cu_seqlens=None, states=None, slots=Non
         raise GdnError("splits must be one to three widths that sum to C")
     n = len(widths)
     if out is None:
-        ys = tuple([x.new_empty((total, c)) for c in widths])
+        ys = _like_parts(x, [(total, c) for c in widths])
         ptrs, strides = _PTRS[n](*[y.data_ptr() for y in ys]), _LONGS[n](*widths)
         begin = _INTS[n + 1](0, *accumulate(widths))
     else:
@@ -820,9 +834,8 @@ def rms_norm_bwd(dy, x, weight, gate=None, d_res=None, eps: float = 1e-6, worksp
     wp = _param(weight, "weight", (D,), dtype, dev)
     gp, gs = _norm_rows(gate, "gate", shape, dtype, dev) if gate is not None else (None, 0)
     dp, ds = _norm_rows(d_res, "d_res", shape, dtype, dev) if d_res is not None else (None, 0)
-    dx = x.new_empty(shape)
+    dx, dgate = _like_parts(x, (shape, shape)) if gate is not None else (x.new_empty(shape), None)
     dw = x.new_empty((D,), dtype=torch.float32)
-    dgate = x.new_empty(shape) if gate is not None else None
     ws, nbytes = _scratch(LIB.gdn_rms_norm_bwd_workspace_size(tokens, heads, D), workspace, x, dev)
     st = _call(dev, LIB.gdn_rms_norm_bwd, yp, xp, wp, gp, dp, dx.data_ptr(), dw.data_ptr(),
                dgate.data_ptr() if dgate is not None else None, tokens, heads, D, ys, xs, gs, ds,

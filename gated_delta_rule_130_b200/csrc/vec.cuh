@@ -70,8 +70,14 @@ __device__ __forceinline__ void store_vec(T *p, const float (&x)[1]) { *p = from
 template <typename T, int VEC>
 __device__ __forceinline__ void load_param(const void *p, long long at, bool f32, float (&x)[VEC]) {
     if (f32) {
+        constexpr int V = VEC % 4 ? 1 : 4;  // `at` is a multiple of VEC
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) x[i] = static_cast<const float *>(p)[at + i];
+        for (int i = 0; i < VEC; i += V) {
+            float v[V];
+            load_vec<float, V>(static_cast<const float *>(p) + at + i, v);
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[i + e] = v[e];
+        }
     } else {
         load_vec<T, VEC>(static_cast<const T *>(p) + at, x);
     }
