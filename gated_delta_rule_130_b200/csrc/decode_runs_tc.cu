@@ -113,6 +113,34 @@ decode_chunks_tc_kernel(RunsArgs a, int row_blocks) {
     const int r0 = row0 + warp * 16 + g, r1 = r0 + 8;  // this lane's rows
     const bool in0 = r0 < a.Dv, in1 = r1 < a.Dv;
     float *state = a.states + ((long long)(run ? slot : 0) * a.Hv + h) * a.Dv * DK + 4 * t;
+    // piece i of the tokens from c0 on: 8 channels of a token's k or q
+    const auto load_piece = [&](int c0, int i) {
+        const int j = i / (2 * KS) % kTok, q = i / (2 * KS * kTok);
+        if (c0 + j >= t1 || (q && !qp)) return make_uint4(0, 0, 0, 0);
+        return *reinterpret_cast<const uint4 *>(
+            (q ? qp + (c0 + j) * a.q_stride : kp + (c0 + j) * a.k_stride) + 8 * (i % (2 * KS)));
+    };
+    // v of this lane's rows and tokens
+    const auto load_v = [&](int c0, float (&v)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = 2 * t + i % 2;
+            v[i] = run && c0 + j < t1 && (i < 2 ? in0 : in1)
+                       ? to_f32(vp[(c0 + j) * a.v_stride + (i < 2 ? r0 : r1)]) : 0.f;
+        }
+    };
+    // the first tokens' loads go ahead of the state's, which the tokens' products do not
+    // wait for
+    uint4 piece = make_uint4(0, 0, 0, 0);
+    float v[4], g0 = 0.f, g1 = 0.f;
+    if (run) {
+        piece = load_piece(t0, tid);
+        if (tid < kTok && t0 + tid < t1) {
+            g0 = a.log_alpha[(t0 + tid) * a.la_stride + h];
+            g1 = a.beta[(t0 + tid) * a.be_stride + h];
+        }
+    }
+    load_v(t0, v);
     float4 s[2][KS];
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
@@ -124,31 +152,25 @@ decode_chunks_tc_kernel(RunsArgs a, int row_blocks) {
 
     for (int c0 = t0; c0 < t1; c0 += kTok) {
         const int m = min(kTok, t1 - c0);
-        float v[4];  // v of this lane's rows and tokens, needed last
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = 2 * t + i % 2;
-            v[i] = run && j < m && (i < 2 ? in0 : in1)
-                       ? to_f32(vp[(c0 + j) * a.v_stride + (i < 2 ? r0 : r1)]) : 0.f;
+        if (c0 > t0) {
+            load_v(c0, v);
+            __syncthreads();  // the arrays are written again
         }
-        if (c0 > t0) __syncthreads();  // the arrays are written again
-        for (int i = tid; i < 2 * kTok * 2 * KS && run; i += blockDim.x) {  // 8 channels each
-            const int j = i / (2 * KS) % kTok, piece = i % (2 * KS), q = i / (2 * KS * kTok);
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (j < m && (!q || qp))
-                x = *reinterpret_cast<const uint4 *>(
-                    (q ? qp + (c0 + j) * a.q_stride : kp + (c0 + j) * a.k_stride) + 8 * piece);
-            uint32_t *to = reinterpret_cast<uint32_t *>(&tok[q][j][16 * (piece / 2)]) + 2 * (piece % 2);
+        for (int i = tid; i < 2 * kTok * 2 * KS && run; i += blockDim.x) {
+            const int j = i / (2 * KS) % kTok, at = i % (2 * KS), q = i / (2 * KS * kTok);
+            const uint4 x = c0 == t0 && i == tid ? piece : load_piece(c0, i);
+            uint32_t *to = reinterpret_cast<uint32_t *>(&tok[q][j][16 * (at / 2)]) + 2 * (at % 2);
             to[0] = x.x;
             to[4] = x.y;
             to[1] = x.z;
             to[5] = x.w;
         }
         if (tid < kTok && run) {
-            float2 gp = make_float2(1.f, 0.f);
-            if (tid < m)
-                gp = decay_pair(a.log_alpha[(c0 + tid) * a.la_stride + h],
-                                a.beta[(c0 + tid) * a.be_stride + h], a.flags);
+            if (c0 > t0 && tid < m) {
+                g0 = a.log_alpha[(c0 + tid) * a.la_stride + h];
+                g1 = a.beta[(c0 + tid) * a.be_stride + h];
+            }
+            const float2 gp = tid < m ? decay_pair(g0, g1, a.flags) : make_float2(1.f, 0.f);
             al[tid] = gp.x;
             be[tid] = gp.y;
         }
