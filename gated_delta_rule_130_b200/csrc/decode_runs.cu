@@ -28,7 +28,7 @@
 // (token by token 412 us).  bf16 runs of Dk = 64 or 128 go to decode_runs_tc.cu.  Where
 // the two meet, us for 1 / 2 / 3 tokens of 256 sequences of 16 heads of 128 x 128:
 // float32 token by token 90 / 129 / 177, up to 8 at once 107 / 116 / 124; bf16 89 / 133 /
-// 185 and 133 / 137 / 139.
+// 185 and about 120 for any number.
 #include "runs_common.cuh"
 
 namespace gdn {
@@ -531,10 +531,11 @@ Cover cover(const RunsArgs &a, int rows) {
     return c;
 }
 
-// Two tokens per sequence or more on average (a batch's rows behind its last sequence
-// count too): up to 8 tokens at once, else token by token.  (The figures are above; the
-// host knows the sizes alone, not the offsets.)
-bool many_tokens(const RunsArgs &a) { return a.total >= 2ll * a.N + 4; }
+// About two tokens per sequence or more on average: up to 8 tokens at once, else token by
+// token.  The figures are above; the host knows the sizes alone, not the offsets, and a
+// batch's rows behind its last sequence count too, which the 4 allows for (one sequence
+// of one token: 3.5 us token by token, 5.4 us by chunks).
+bool many_tokens(const RunsArgs &a) { return a.total >= 2ll * a.N - a.N / 8 + 4; }
 
 template <typename T, int K>
 cudaError_t launch_t(const RunsArgs &a, cudaStream_t st) {

@@ -14,15 +14,17 @@
 // update.  8 x 8 token products are far too small for a tcgen05 tile of 64 or 128 rows
 // with its round trip through tensor memory.
 //
-// 64 runs of 1 to 8 tokens against 32 value heads of 128 x 128 (read only, 135 MB): 49.4
-// us on B200, 0.42 of the measured copy rate (in float32 arithmetic 61.5 us); 8 tokens of
-// 64 sequences of 16 heads, states written, 143 MB: 35.2 us.  Two blocks of 128 registers
-// a thread per SM; what bounds it is the chain of one part of the work - offsets and
-// slot, k and q, the tokens' products and the substitution on one warp, the outputs - with
-// only 16 warps to hide it: without the tokens' products it takes 26 us.  Tried and
-// slower: every warp forming T and M for itself (55.6 us), a ninth warp for them (67),
-// blocks that stay and copy the next rows ahead (53.8), blocks of 4 warps (50.4), 3
-// blocks of 80 registers (56.5).
+// 64 runs of 1 to 8 tokens against 32 value heads of 128 x 128 (read only, 135 MB): 42.4
+// us on B200, 0.49 of the measured copy rate (in float32 arithmetic 61.5 us); 8 tokens of
+// 256 sequences of 16 heads, states written, 571 MB: 122.5 us, 0.71.  Two blocks of 128
+// registers a thread per SM; what bounds it is the chain of one part of the work -
+// offsets and slot, k and q, the tokens' products and the substitution on one warp, the
+// outputs - with only 16 warps to hide it.  The tokens' loads go ahead of the state's:
+// behind them they came 2 us later (49.4 us).  Tried and slower, against 49.4: every warp
+// forming T and M for itself (55.6), a ninth warp for them (67), blocks of 4 warps (50.4),
+// 3 blocks of 80 registers (56.5), blocks that stay and copy the next part's rows and
+// tokens ahead (58.8: the copies' issue waits as long as the loads did), the next round's
+// rows fetched into L2 (49.6).
 //
 // A state with an infinity gives NaN in its row, where the recurrence might give an
 // infinity.
