@@ -24,7 +24,7 @@
 // state being read and written once; one token each of 256 sequences of 16 heads of
 // 128 x 128, 541 MB: 93.0 us on B200, 0.89 of the measured copy rate.  Up to 8 tokens at
 // once, for longer runs: bound by the issue of its products' reductions and by the
-// barriers between its phases; 8 tokens of 256 sequences of 16 heads in float32: 194 us
+// barriers between its phases; 8 tokens of 256 sequences of 16 heads in float32: 182 us
 // (token by token 412 us).  bf16 runs of Dk = 64 or 128 go to decode_runs_tc.cu.  Where
 // the two meet, us for 1 / 2 / 3 tokens of 256 sequences of 16 heads of 128 x 128:
 // float32 token by token 90 / 129 / 177, up to 8 at once 107 / 116 / 124; bf16 89 / 133 /
@@ -554,11 +554,14 @@ cudaError_t launch_t(const RunsArgs &a, cudaStream_t st) {
         else if (a.Dk <= 128) GDN_RUNS(decode_tokens_kernel, 32, 4, 1);
         else GDN_RUNS(decode_tokens_kernel, 32, 2, 2);
     } else {
+        // (two float4 per lane and four rows per lane group: 8 float32 tokens of 256
+        // sequences of 16 heads of 128 x 128 182 us, four float4 and two rows 196 us; of
+        // 4 heads of 256 x 256 157 and 172 us)
         if (a.Dk <= 16) GDN_RUNS(decode_chunks_kernel, 4, 4, 1);
-        else if (a.Dk <= 32) GDN_RUNS(decode_chunks_kernel, 4, 4, 2);
-        else if (a.Dk <= 64) GDN_RUNS(decode_chunks_kernel, 4, 2, 4);
-        else if (a.Dk <= 128) GDN_RUNS(decode_chunks_kernel, 8, 2, 4);
-        else GDN_RUNS(decode_chunks_kernel, 16, 2, 4);
+        else if (a.Dk <= 32) GDN_RUNS(decode_chunks_kernel, 8, 4, 1);
+        else if (a.Dk <= 64) GDN_RUNS(decode_chunks_kernel, 8, 4, 2);
+        else if (a.Dk <= 128) GDN_RUNS(decode_chunks_kernel, 16, 4, 2);
+        else GDN_RUNS(decode_chunks_kernel, 32, 4, 2);
     }
 #undef GDN_RUNS
     return cudaPeekAtLastError();
