@@ -118,7 +118,37 @@ __device__ __forceinline__ void silu_grad_vec(const float (&z)[VEC], float (&d)[
 // they lie behind its tile, and no other block does: so the held inputs of a slot are
 // read and written by one thread only.
 constexpr int kMine = 1, kPadding = 2, kFirst = 4, kHold = 8;
-constexpr int kMaxTile = 512;  // tokens per block
+constexpr int kMaxTile = 256;  // tokens per block
+
+// Of the sequences with tokens that name one slot the first has it.  A block asks for all
+// sequences of its tile in one pass over the slots before them: a table in shared memory
+// holds, for each slot that the tile names, the first token that does; a place is the
+// token's index in the tile, kTaken with it once an earlier sequence has named the slot.
+// (The slots before each sequence one after the other: a token each of 4096 sequences of
+// 6144 channels 228 us, so 91 us; without slots 81 us.)
+constexpr int kPlaces = 2 * kMaxTile, kFree = -1, kTaken = 1 << 16;
+struct SlotTable {
+    int place[kPlaces], slot[kMaxTile + 2];  // slot: of each token, -1: none or padding
+
+    // Where `want` stands, or the free place that ends its search.
+    __device__ __forceinline__ int find(int want) const {
+        int i = (int)((unsigned)want * 2654435761u % kPlaces);
+        while (place[i] != kFree && slot[place[i] & (kTaken - 1)] != want) i = (i + 1) % kPlaces;
+        return i;
+    }
+    // Token i names its slot.
+    __device__ __forceinline__ void insert(int i) {
+        const int want = slot[i];
+        for (int at = (int)((unsigned)want * 2654435761u % kPlaces);; at = (at + 1) % kPlaces) {
+            const int old = atomicCAS(&place[at], kFree, i);
+            if (old == kFree) return;
+            if (slot[old] == want) {
+                atomicMin(&place[at], i);
+                return;
+            }
+        }
+    }
+};
 
 // The rows of x come through a ring of shared memory, each thread's own channels by
 // itself, S - 1 groups of B rows ahead.
@@ -134,6 +164,11 @@ conv_fwd(ConvArgs a, unsigned ctiles, int tile) {
     // of the tile's tokens and those behind it: the sequence (-1: none), the flags
     __shared__ int seq[kMaxTile + W - 2];
     __shared__ __align__(8) unsigned char flag[(kMaxTile + W - 2 + 7) / 8 * 8];
+    // the table lies in the ring's last group, which is empty until the tokens are begun, if
+    // it is large enough (more shared memory would take L1 from the copies: 85.4 us)
+    constexpr bool kInRing = sizeof(ring[0]) >= sizeof(SlotTable);
+    __shared__ __align__(16) unsigned char own_table[kInRing ? 16 : sizeof(SlotTable)];
+    SlotTable &table = *reinterpret_cast<SlotTable *>(kInRing ? static_cast<void *>(ring[S - 1]) : own_table);
     const int tid = threadIdx.x, lane = tid % 32;
     const int c = (int)((blockIdx.x % ctiles * kThreads + tid) * VEC);
     const int t0 = (int)(blockIdx.x / ctiles) * tile, t1 = min(t0 + tile, a.total);
@@ -170,10 +205,10 @@ conv_fwd(ConvArgs a, unsigned ctiles, int tile) {
         lo = seq_of(a.cu, a.N, t0, lane);
         hi = seq_of(a.cu, a.N, stop - 1, lane);
     }
-    const int padded = (stop - t0 + 31) / 32 * 32;
-    for (int i = tid; i < padded; i += kThreads) {
+    const bool named = a.states && a.slots;
+    for (int i = tid; i < stop - t0; i += kThreads) {
         const int t = t0 + i;
-        const Span sp = span_of(a, t < stop ? t : -1, lo, hi);
+        const Span sp = span_of(a, t, lo, hi);
         const bool in = sp.start < sp.end;
         int f = 0, slot = -1;
         if (in) {
@@ -183,33 +218,47 @@ conv_fwd(ConvArgs a, unsigned ctiles, int tile) {
             if (pos == 0) f |= kFirst;
             if (a.states) {
                 slot = a.slots ? a.slots[sp.n] : sp.n;
-                if (slot < 0 || slot >= a.n_slots) f |= kPadding;
-                // with the last token that needs them the held inputs give way
-                else if (t == min(sp.start + W - 2, sp.end - 1)) f |= kHold;
+                if (slot < 0 || slot >= a.n_slots) {
+                    f |= kPadding;
+                    slot = -1;
+                } else if (t == min(sp.start + W - 2, sp.end - 1)) {
+                    f |= kHold;  // with the last token that needs them the held inputs give way
+                }
             }
         }
-        if (a.states && a.slots) {
-            // of the sequences with tokens that name one slot the first has it: the warp
-            // looks at the sequences that its 32 tokens begin with or begin
-            const int n = in ? sp.n : -1, before = __shfl_up_sync(0xffffffffu, n, 1);
-            unsigned todo = __ballot_sync(0xffffffffu, in && !(f & kPadding) &&
-                                                           (lane == 0 || before != n));
-            while (todo) {
-                const int k = __ffs(todo) - 1;
-                todo &= todo - 1;
-                const int m = __shfl_sync(0xffffffffu, n, k);
-                const int want = __shfl_sync(0xffffffffu, slot, k);
-                const int taken = slot_taken(a.slots, a.cu, m, want, lane, 32);
-                if (__any_sync(0xffffffffu, taken) && n == m) f |= kPadding;
-            }
-        }
-        if (t < stop) {
-            seq[i] = in ? sp.n : -1;
-            flag[i] = f;
-        }
+        seq[i] = in ? sp.n : -1;
+        flag[i] = f;
+        if (named) table.slot[i] = slot;
     }
     if (tid < 8 && stop - t0 + tid < (int)sizeof(flag)) flag[stop - t0 + tid] = 0;
+    if (named)
+        for (int i = tid; i < kPlaces; i += kThreads) table.place[i] = kFree;
     __syncthreads();
+    if (named) {
+        for (int i = tid; i < stop - t0; i += kThreads)
+            if (table.slot[i] >= 0 && (i == 0 || seq[i - 1] != seq[i])) table.insert(i);
+        __syncthreads();
+        const int last = a.cu ? hi : stop - 1;  // the tile's last sequence
+        for (int m = 4 * tid; m < last; m += 4 * kThreads) {
+            int s[4];
+            load_slots(a.slots, m, last, s);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (s[k] < 0) continue;
+                const int at = table.find(s[k]), held_by = table.place[at];
+                if (held_by >= 0 && held_by < kTaken && m + k < seq[held_by] &&
+                    (!a.cu || a.cu[m + k] < a.cu[m + k + 1]))
+                    atomicOr(&table.place[at], kTaken);
+            }
+        }
+        __syncthreads();
+        for (int i = tid; i < stop - t0; i += kThreads)
+            if (table.slot[i] >= 0) {
+                const int held_by = table.place[table.find(table.slot[i])];
+                if (held_by >= kTaken || seq[held_by] != seq[i]) flag[i] |= kPadding;
+            }
+        __syncthreads();
+    }
     if (!live) return;
     int count = t1 - t0;
     for (int i = t1 - t0; i < stop - t0; ++i)
@@ -400,7 +449,7 @@ conv_few(ConvArgs a, unsigned ctiles) {
 
 // Blocks of the backward per SM: 4 of 120 registers a thread (5 of 96 spill, and took
 // 163.5 us on 16384 x 6144 where these take 119.0 us).
-constexpr int kBwdPerSM = 4;
+constexpr int kBwdPerSM = 4, kMaxBwdTile = 512;
 
 // Backward.  A block: kThreads * VEC channels and the tokens [t0, t0 + tile): their dx
 // (dz of the W - 1 tokens behind the tile is formed again) and their share of dw.
@@ -414,7 +463,7 @@ conv_bwd(ConvArgs a, unsigned ctiles, int tile) {
     const int tid = threadIdx.x;
     // of each token of the tile and behind it: how many inputs of its sequence lie
     // before it (W - 1 at most), -1 where it is in none
-    __shared__ __align__(4) signed char before[kMaxTile + W - 1];
+    __shared__ __align__(4) signed char before[kMaxBwdTile + W - 1];
     const int lane = threadIdx.x % 32;
     const int c = (int)((blockIdx.x % ctiles * kThreads + threadIdx.x) * VEC);
     const int t0 = (int)(blockIdx.x / ctiles) * tile, t1 = min(t0 + tile, a.total);
@@ -621,19 +670,21 @@ bool vectors_fit(const ConvArgs &a) {
 unsigned channel_tiles(int C, int vec) { return (C + kThreads * vec - 1) / (kThreads * vec); }
 
 // Tokens per block such that `per_sm` blocks per SM take them all at once, at least 8.
-int tile_of(int total, unsigned ctiles, int per_sm) {
+int tile_of(int total, unsigned ctiles, int per_sm, int most) {
     const int rows = 148 * per_sm / (int)ctiles > 1 ? 148 * per_sm / (int)ctiles : 1;
     const int tile = ((total + rows - 1) / rows + 7) / 8 * 8;
-    return tile > kMaxTile ? kMaxTile : tile;
+    return tile > most ? most : tile;
 }
 
 template <typename T, int VEC, int W>
 cudaError_t fwd_w(const ConvArgs &a, cudaStream_t st) {
     const unsigned ct = channel_tiles(a.C, VEC);
-    if ((long long)ct * a.total <= 148 * 32) {
+    // (each warp of conv_few looks at the slots for itself: a token each of 4096 sequences of
+    // 512 channels 20.6 us, with the tiles 16.4 us; of 1024 sequences 6.6 and 6.4 us)
+    if ((long long)ct * a.total <= 148 * 32 && !(a.slots && a.N > 1024)) {
         conv_few<T, VEC, W><<<ct * a.total, kThreads, 0, st>>>(a, ct);
     } else {
-        const int tile = tile_of(a.total, ct, kFwdPerSM<T, VEC>);
+        const int tile = tile_of(a.total, ct, kFwdPerSM<T, VEC>, kMaxTile);
         conv_fwd<T, VEC, W><<<ct * ((a.total + tile - 1) / tile), kThreads, 0, st>>>(a, ct, tile);
     }
     return cudaPeekAtLastError();
@@ -641,7 +692,7 @@ cudaError_t fwd_w(const ConvArgs &a, cudaStream_t st) {
 
 // The backward's tile.  Sized for vectors of 4 channels whatever
 // the call's alignment and type are, so that the workspace depends on the sizes alone.
-int bwd_tile(int total, int C) { return tile_of(total, channel_tiles(C, 4), kBwdPerSM); }
+int bwd_tile(int total, int C) { return tile_of(total, channel_tiles(C, 4), kBwdPerSM, kMaxBwdTile); }
 
 template <typename T, int VEC, int W>
 cudaError_t bwd_w(const ConvArgs &a, cudaStream_t st) {

@@ -194,21 +194,25 @@ __device__ __forceinline__ void fast_sigmoid(const float (&x)[VEC], float (&s)[V
     }
 }
 
-// Whether one of the sequences before n that have tokens names `slot`; each caller looks
-// at its share, four slots (16 bytes aligned) at once.
+// slots[i .. i + 3], i a multiple of 4, from an array 16 bytes aligned; -1 from n on.
+__device__ __forceinline__ void load_slots(const int *slots, int i, int n, int (&s)[4]) {
+    if (i + 4 <= n) {
+        const int4 v = *reinterpret_cast<const int4 *>(slots + i);
+        s[0] = v.x; s[1] = v.y; s[2] = v.z; s[3] = v.w;
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[k] = i + k < n ? slots[i + k] : -1;
+}
+// Whether one of the sequences before n that have tokens names `slot` (>= 0); each caller
+// looks at its share.
 __device__ __forceinline__ int slot_taken(const int *slots, const int *cu, int n, int slot, int from,
                                           int step) {
     int taken = 0;
 #pragma unroll 2
     for (int i = 4 * from; i < n; i += 4 * step) {
         int s[4];
-        if (i + 4 <= n) {
-            const int4 v = *reinterpret_cast<const int4 *>(slots + i);
-            s[0] = v.x; s[1] = v.y; s[2] = v.z; s[3] = v.w;
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) s[k] = i + k < n ? slots[i + k] : slot ^ 1;
-        }
+        load_slots(slots, i, n, s);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if (s[k] == slot) taken |= !cu || cu[i + k] < cu[i + k + 1];

@@ -113,6 +113,26 @@ def test_padding_rows_behind_and_a_slot_twice(gdn):
     assert (y[cu[1]:cu[3]] == 0).all() and (y[cu[4]:cu[5]] == 0).all()
 
 
+@pytest.mark.parametrize("kind", ["tokens", "ragged", "long", "one slot"])
+def test_many_sequences_slots_again(gdn, kind):
+    # slots named again inside a tile, tiles apart, by sequences with and without tokens
+    g = torch.Generator().manual_seed(12)
+    n, C = 2500, 1024
+    lens = [1] * n
+    if kind == "ragged":
+        lens = torch.randint(0, 6, (n,), generator=g).tolist()
+    if kind == "long":
+        n, lens = 9, [700, 0, 3, 700, 1, 1, 2, 900, 300]
+    slots = torch.randint(-1, n // 2, (n,), generator=g)
+    slots[slots % 7 == 3] += n  # some out of the pool
+    if kind == "one slot":
+        slots[:] = 5
+    if kind == "long":
+        slots = torch.tensor([3, 2, 2, 3, -1, 1, 2, 2, 0])
+    d = draw(sum(lens), C, 4, n // 2, BF16, 12, bias=False)
+    check_fwd(gdn, d, offsets(lens) if kind != "tokens" else None, slots.tolist())
+
+
 def test_prompt_then_tokens(gdn):
     # a prompt, then its continuation one token at a time, is the whole sequence at once
     for dtype in (F32, BF16):
