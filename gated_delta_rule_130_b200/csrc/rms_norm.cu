@@ -58,7 +58,7 @@ __device__ __forceinline__ float row_reduce(float x, float *part) {
 }
 
 __device__ __forceinline__ float quant_inverse(float top, float *scale) {
-    top = max_nan(top, kTinyMax);
+    top = max_nan(fmaf(top, 0.f, top), kTinyMax);  // an infinity becomes NaN
     *scale = top * (1.f / kE4M3Max);
     return kE4M3Max / top;
 }

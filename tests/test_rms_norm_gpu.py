@@ -98,6 +98,39 @@ def test_nan_and_infinity_stay_in_their_rows(gdn):
         assert torch.isfinite(dx[[0, 2, 4, 5]].float()).all() and dx[1].isnan().all()
 
 
+@pytest.mark.parametrize("dtype,D", [(F32, 256), (BF16, 1024), (F32, 131), (BF16, 384), (BF16, 40064)])
+def test_an_infinite_value_in_8_bits(gdn, dtype, D):
+    # no scale holds an infinity: the scale and the values of its row or group are NaN
+    d = draw((5, D), dtype, 11)
+    d["gate"][2, 3] = float("inf")
+    for quant in ("row", "group") if D % 128 == 0 else ("row",):
+        y, scale, _ = gdn.rms_norm_fwd(d["x"], d["w"], gate=d["gate"], quant=quant)
+        n = D if quant == "row" else 128
+        y = y.float()
+        assert scale[2, 0].isnan() and y[2, :n].isnan().all()
+        assert torch.isfinite(y[[0, 1, 3, 4]]).all() and torch.isfinite(scale[[0, 1, 3, 4]]).all()
+        assert torch.isfinite(y[2, n:]).all() and torch.isfinite(scale[2, 1:]).all()
+
+
+def test_rows_beyond_32_bit_offsets(gdn):
+    # 2.2e9 elements, all zero but the last rows
+    rows, D = 270_000, 8192
+    x = torch.zeros(rows, D, dtype=BF16, device="cuda")
+    dy = torch.zeros_like(x)
+    d = draw((6, D), BF16, 12)
+    x[-6:], dy[-6:] = d["x"], d["dy"]
+    y, scale, _ = gdn.rms_norm_fwd(x, d["w"], quant="group")
+    z, zs, _ = gdn.rms_norm_fwd(d["x"], d["w"], quant="group")
+    assert torch.equal(y[-6:].float(), z.float()) and torch.equal(scale[-6:], zs)
+    assert not (y[:-6].view(torch.uint8) & 0x7f).any()  # +0 or -0, as the weight
+    del y, scale
+    dx, dw, _ = gdn.rms_norm_bwd(dy, x, d["w"])
+    ex, ew, _ = gdn.rms_norm_bwd(d["dy"], d["x"], d["w"])
+    assert torch.equal(dx[-6:], ex) and not dx[:-6].any()
+    ref = R.norm_grads(d["dy"], d["x"], d["w"], None, None, EPS)
+    R.close(dw, ref[1], ref[4], bwd_roundings(D, 6))
+
+
 def test_gate_at_its_ends(gdn):
     d = draw((4, 128), F32, 4)
     d["gate"][0], d["gate"][1], d["gate"][2] = -200.0, 200.0, 0.0
