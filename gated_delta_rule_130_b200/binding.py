@@ -479,6 +479,15 @@ def decode_step(q, k, v, log_alpha, beta, S, out=None, l2norm_qk: bool = False,
 GDN_FLAG_READ_ONLY = 4
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _ints(*sizes):
+    """The C entry points count in 32-bit integers; ctypes would cut larger sizes off."""
+    if max(sizes) > _INT_MAX:
+        raise GdnError(f"a size above {_INT_MAX} is not supported")
+
+
 def _cuda(t, name: str) -> int:
     """Index of the CUDA device that tensor ``t`` is on."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -563,6 +572,7 @@ def _sequences(cu_seqlens, slots, total, dev: int):
         if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
             raise GdnError("cu_seqlens must hold N + 1 offsets")
         N = cu_seqlens.shape[0] - 1
+        _ints(N)
     if slots is not None:
         sl = _dense(slots, "slots", torch.int32, dev)
         if slots.shape != (N,):
@@ -605,6 +615,7 @@ def decode_runs(q, k, v, log_alpha, beta, states, slots=None, cu_seqlens=None, o
     if Hk == 0 or Hv % Hk:
         raise GdnError("Hv must be a multiple of Hk")
     n_slots = states.shape[0]
+    _ints(total, Hk, Hv, Dk, Dv, n_slots)
     kp, ks = _rows(k, "k", dtype, dev)
     qp, qs = _rows(q, "q", dtype, dev) if q is not None else (None, 0)
     vp, vs = _rows(v, "v", dtype, dev)
@@ -682,6 +693,7 @@ def short_conv_fwd(x, weight, bias=None, cu_seqlens=None, states=None, slots=Non
         if slots is None and N > n_slots:
             raise GdnError("without slots, states must hold one state per sequence")
         sp = _dense(states, "states", dtype, dev)
+    _ints(total, C, W, n_slots)
     widths = [C] if splits is None else list(splits)
     if not 1 <= len(widths) <= 3 or sum(widths) != C or min(widths) <= 0:
         raise GdnError("splits must be one to three widths that sum to C")
@@ -725,6 +737,7 @@ def short_conv_bwd(dy, x, weight, bias=None, cu_seqlens=None, silu: bool = True,
         if bias.dtype is not weight.dtype:
             raise GdnError("bias and weight must have one type")
         bp = _param(bias, "bias", (C,), dtype, dev)
+    _ints(total, C, W)
     cu, _, N = _sequences(cu_seqlens, None, total, dev)
     dys = (dy,) if isinstance(dy, torch.Tensor) else tuple(dy)
     widths = [d.shape[1] for d in dys if d.dim() == 2]
@@ -764,6 +777,7 @@ def _norm_sizes(shape):
     tokens = 1
     for n in shape[:-2] if len(shape) > 2 else shape[:-1]:
         tokens *= n
+    _ints(tokens, heads, shape[-1])
     return tokens, heads, shape[-1]
 
 

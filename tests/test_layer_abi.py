@@ -192,6 +192,17 @@ def test_binding_refuses_bad_shapes_and_cpu_tensors():
             f()
 
 
+def test_binding_refuses_sizes_beyond_32_bits():
+    # ctypes would cut 2^32 + 5 rows down to 5
+    from gated_delta_rule_130_b200 import binding as b
+    assert b._norm_sizes((2 ** 20, 4, 64)) == (2 ** 20, 4, 64)
+    for shape in ((2 ** 32 + 5, 1), (1, 2 ** 32 + 8), (2 ** 16, 2 ** 16, 2, 8), (2, 2 ** 31, 8)):
+        with pytest.raises(b.GdnError):
+            b._norm_sizes(shape)
+    with pytest.raises(b.GdnError):
+        b._ints(4, 2 ** 31)
+
+
 STUBS = r"""
 #include <cuda_runtime.h>
 #include "kernels.h"

@@ -241,6 +241,26 @@ def test_gradients_against_differences(gdn):
     assert (slope - mine).abs() <= 1e-5 * size  # differences: 1e-10 + 1e-11; float32: 90 u32
 
 
+def test_tokens_beyond_32_bit_offsets(gdn):
+    # 2.2e9 elements, all zero but the last tokens, which are two sequences
+    total, C, n = 270_000, 8192, 40
+    d = draw(n, C, 4, 2, BF16, 13)
+    x = torch.zeros(total, C, dtype=BF16, device="cuda")
+    dy = torch.zeros_like(x)
+    x[-n:], dy[-n:] = d["x"], d["dy"]
+    cu, some = dev([0, total - n, total - 7, total]), [0, n - 7, n]
+    S, T = d["states"][[0, 0, 1]].clone(), d["states"].clone()
+    y = gdn.short_conv_fwd(x, d["w"], cu_seqlens=cu, states=S)
+    z = gdn.short_conv_fwd(d["x"], d["w"], cu_seqlens=dev(some), states=T)
+    assert torch.equal(y[-n:], z) and torch.equal(S[1:], T) and not S[0].any()
+    del y
+    dx, dw, _ = gdn.short_conv_bwd(dy, x, d["w"], cu_seqlens=cu)
+    assert not dx[:-n].any()
+    rx, rw, _, sx, sw, _ = R.conv_grads(d["dy"], d["x"], d["w"], None, some, True)
+    R.close(dx[-n:], rx, sx, bwd_roundings(n))
+    R.close(dw, rw, sw, bwd_roundings(n))
+
+
 def test_no_tokens(gdn):
     d = draw(0, 16, 4, 1, F32, 11)
     for cu in ([0], [0, 0], None):
