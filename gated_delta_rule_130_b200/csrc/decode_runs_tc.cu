@@ -24,7 +24,9 @@
 // forming T and M for itself (55.6), a ninth warp for them (67), blocks of 4 warps (50.4),
 // 3 blocks of 80 registers (56.5), blocks that stay and copy the next part's rows and
 // tokens ahead (58.8: the copies' issue waits as long as the loads did), the next round's
-// rows fetched into L2 (49.6).
+// rows fetched into L2 (49.6).  Against 42.4: blocks that stay, the next part's rows by one
+// bulk copy of 64 KB (57.8, one per SM without spills 65.4: twice the instructions, and the
+// barriers' waits stay).
 //
 // A state with an infinity gives NaN in its row, where the recurrence might give an
 // infinity.
