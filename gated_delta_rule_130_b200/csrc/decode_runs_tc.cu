@@ -26,7 +26,10 @@
 // tokens ahead (58.8: the copies' issue waits as long as the loads did), the next round's
 // rows fetched into L2 (49.6).  Against 42.4: blocks that stay, the next part's rows by one
 // bulk copy of 64 KB (57.8, one per SM without spills 65.4: twice the instructions, and the
-// barriers' waits stay).
+// barriers' waits stay).  A kernel for read-only runs alone, 3 blocks of 80 registers that hold
+// three of the eight steps of a row at a time, took 40.8 (and 78.7 instead of 85.2 at 256
+// sequences of 16 heads), but spills where such a run is longer than 8 tokens; the split
+// into three parts and its products are then what it waits for (one part alone: 34).
 //
 // A state with an infinity gives NaN in its row, where the recurrence might give an
 // infinity.
