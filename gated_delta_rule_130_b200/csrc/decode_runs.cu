@@ -537,10 +537,14 @@ Cover cover(const RunsArgs &a, int rows) {
 }
 
 // About two tokens per sequence or more on average: up to 8 tokens at once, else token by
-// token.  The figures are above; the host knows the sizes alone, not the offsets, and a
-// batch's rows behind its last sequence count too, which the 4 allows for (one sequence
-// of one token: 3.5 us token by token, 5.4 us by chunks).
-bool many_tokens(const RunsArgs &a) { return a.total >= 2ll * a.N - a.N / 8 + 4; }
+// token.  The figures are above and, for few sequences (us token by token and at once, bf16,
+// 16 heads of 128 x 128): 8 of 2 tokens 8.2 and 7.1 (float32 7.7 and 7.1), one of 1 token 3.5
+// and 6.6, of 3 6.6 and 6.8, of 4 8.1 and 6.9.  The host knows the sizes alone, not the
+// offsets, and a batch's rows behind its last sequence count too: for few sequences, of
+// which they can be most, the 4 allows for them.
+bool many_tokens(const RunsArgs &a) {
+    return a.total >= 2ll * a.N - a.N / 8 + (a.N < 8 ? 4 : 1);
+}
 
 template <typename T, int K>
 cudaError_t launch_t(const RunsArgs &a, cudaStream_t st) {

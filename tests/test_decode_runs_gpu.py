@@ -103,7 +103,8 @@ def test_raw_inputs(gdn, dtype):
 # the kernels: runs of several tokens in float32 (at a vector and an odd width) and in bf16
 # on the tensor cores, and batches of single tokens (token by token)
 KERNELS = [(F32, 32, 24, [3, 2, 1, 9]), (F32, 37, 24, [3, 2, 1, 9]), (BF16, 128, 40, [3, 2, 1, 9]),
-           (BF16, 64, 136, [8, 2, 1, 17]), (F32, 128, 24, [1, 1, 1, 1]), (BF16, 72, 24, [2, 1, 1, 1])]
+           (BF16, 64, 136, [8, 2, 1, 17]), (F32, 128, 24, [1, 1, 1, 1]), (BF16, 72, 24, [2, 1, 1, 1]),
+           (BF16, 72, 24, [1, 1, 1, 1])]
 
 
 @pytest.mark.parametrize("dtype,Dk,Dv,lens", KERNELS)
