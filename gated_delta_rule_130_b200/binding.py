@@ -555,12 +555,13 @@ def _like_parts(x, shapes):
 
 
 def _scratch(need: int, workspace, like, dev: int):
-    """Pointer and bytes of the workspace, a new one where none or too small a one is given."""
-    if workspace is not None:
-        nbytes = workspace.numel() * workspace.element_size()
-        if nbytes >= need:
-            return _dense(workspace, "workspace", workspace.dtype, dev), nbytes
-    return like.new_empty(max(need, 16), dtype=torch.uint8).data_ptr(), max(need, 16)
+    """The workspace (a new one where none or too small a one is given), its pointer and its
+    bytes.  The caller holds the tensor until the entry point has returned: an allocator may
+    give the memory of one that nobody holds to another thread before the kernels are launched."""
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = like.new_empty(max(need, 16), dtype=torch.uint8)
+    return (workspace, _dense(workspace, "workspace", workspace.dtype, dev),
+            workspace.numel() * workspace.element_size())
 
 
 def _sequences(cu_seqlens, slots, total, dev: int):
@@ -747,7 +748,8 @@ def short_conv_bwd(dy, x, weight, bias=None, cu_seqlens=None, silu: bool = True,
     dx = x.new_empty((total, C))
     dw = x.new_empty((C, W), dtype=torch.float32)
     db = x.new_empty((C,), dtype=torch.float32) if bias is not None else None
-    ws, nbytes = _scratch(LIB.gdn_short_conv_bwd_workspace_size(total, C, W), workspace, x, dev)
+    workspace, ws, nbytes = _scratch(LIB.gdn_short_conv_bwd_workspace_size(total, C, W), workspace,
+                                     x, dev)
     st = _call(dev, LIB.gdn_short_conv_bwd, ptrs, strides, begin, len(dys), xp, wp, bp, cu,
                dx.data_ptr(), dw.data_ptr(), db.data_ptr() if db is not None else None, N, total,
                C, W, xs, int(silu), code, _dtype_code(weight), ws, nbytes)
@@ -850,7 +852,8 @@ def rms_norm_bwd(dy, x, weight, gate=None, d_res=None, eps: float = 1e-6, worksp
     dp, ds = _norm_rows(d_res, "d_res", shape, dtype, dev) if d_res is not None else (None, 0)
     dx, dgate = _like_parts(x, (shape, shape)) if gate is not None else (x.new_empty(shape), None)
     dw = x.new_empty((D,), dtype=torch.float32)
-    ws, nbytes = _scratch(LIB.gdn_rms_norm_bwd_workspace_size(tokens, heads, D), workspace, x, dev)
+    workspace, ws, nbytes = _scratch(LIB.gdn_rms_norm_bwd_workspace_size(tokens, heads, D), workspace,
+                                     x, dev)
     st = _call(dev, LIB.gdn_rms_norm_bwd, yp, xp, wp, gp, dp, dx.data_ptr(), dw.data_ptr(),
                dgate.data_ptr() if dgate is not None else None, tokens, heads, D, ys, xs, gs, ds,
                eps, code, _dtype_code(weight), ws, nbytes)

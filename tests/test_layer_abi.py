@@ -285,3 +285,42 @@ def test_entry_points_under_address_and_undefined_behaviour_sanitizers(tmp_path)
     run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
     assert run.returncode == 0 and "sanitized layer ABI ok" in run.stdout, \
         (run.stdout + run.stderr)[-3000:]
+
+
+@pytest.mark.parametrize("given", [None, 16])
+def test_what_a_call_allocates_lives_until_the_entry_point_returns(monkeypatch, given):
+    # a stand-in for the C entry points looks whether every array that the binding made for
+    # the call, the workspace among them, still belongs to someone while it runs
+    import weakref
+
+    from gated_delta_rule_130_b200 import binding as b
+    made, passed = [], []
+    real = torch.Tensor.new_empty
+
+    def new_empty(self, *a, **kw):
+        t = real(self, *a, **kw)
+        made.append((weakref.ref(t), t.data_ptr()))
+        return t
+
+    def entry(*args):
+        for alive, ptr in made:
+            assert alive() is not None, "an array was given up before the launch"
+            passed.append(ptr in args)
+        return 0
+
+    class Lib:
+        gdn_short_conv_bwd = gdn_rms_norm_bwd = staticmethod(entry)
+        gdn_short_conv_bwd_workspace_size = gdn_rms_norm_bwd_workspace_size = staticmethod(lambda *s: 4096)
+
+    monkeypatch.setattr(b, "LIB", Lib)
+    monkeypatch.setattr(b, "_cuda", lambda t, name: t.get_device())
+    monkeypatch.setattr(b, "_call", lambda dev, f, *args: f(*args, None))
+    monkeypatch.setattr(torch.Tensor, "new_empty", new_empty)
+    z = torch.zeros
+    ws = None if given is None else z(given, dtype=torch.uint8)  # one that is too small
+    b.short_conv_bwd(z(4, 8), z(4, 8), z(8, 4), z(8), cu_seqlens=z(2, dtype=torch.int32), workspace=ws)
+    assert passed == [True] * 4  # dx, dweight, dbias, workspace
+    made.clear()
+    passed.clear()
+    b.rms_norm_bwd(z(4, 8), z(4, 8), z(8), workspace=ws)
+    assert passed == [True] * 3  # dx, dweight, workspace

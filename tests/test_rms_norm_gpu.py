@@ -238,3 +238,14 @@ def test_no_rows_and_graphs(gdn):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(out, both()))
+
+
+def test_a_given_workspace(gdn):
+    # the same bits, nothing behind its size written; one that is too small is not used
+    d = draw((300, 3, 96), BF16, 13)
+    a = gdn.rms_norm_bwd(d["dy"], d["x"], d["w"], gate=d["gate"])
+    need = gdn.rms_norm_bwd_workspace_size(300, 3, 96)
+    for size in (need, 16):
+        ws = torch.full((need + 64,), 7, dtype=torch.uint8, device="cuda")
+        b = gdn.rms_norm_bwd(d["dy"], d["x"], d["w"], gate=d["gate"], workspace=ws[:size])
+        assert all(torch.equal(s, t) for s, t in zip(a, b)) and (ws[size:] == 7).all()

@@ -270,3 +270,15 @@ def test_no_tokens(gdn):
     d = draw(4, 16, 4, 1, F32, 11)  # tokens, but no sequence
     dx, dw, db = gdn.short_conv_bwd(d["dy"], d["x"], d["w"], d["b"], cu_seqlens=dev([0]))
     assert (dx == 0).all() and (dw == 0).all() and (db == 0).all()
+
+
+def test_a_given_workspace(gdn):
+    # the same bits, nothing behind its size written; one that is too small is not used
+    d = draw(700, 96, 4, 1, BF16, 22)
+    cu = dev([0, 300, 700])
+    a = gdn.short_conv_bwd(d["dy"], d["x"], d["w"], d["b"], cu_seqlens=cu)
+    need = gdn.short_conv_bwd_workspace_size(700, 96, 4)
+    for size in (need, 16):
+        ws = torch.full((need + 64,), 7, dtype=torch.uint8, device="cuda")
+        b = gdn.short_conv_bwd(d["dy"], d["x"], d["w"], d["b"], cu_seqlens=cu, workspace=ws[:size])
+        assert all(torch.equal(s, t) for s, t in zip(a, b)) and (ws[size:] == 7).all()
