@@ -246,7 +246,7 @@ decode_tokens_kernel(RunsArgs a, int row_blocks, int tiles) {
                 }
                 const float g0 = a.log_alpha[t * a.la_stride + h], g1 = a.beta[t * a.be_stride + h];
                 if (t == t0 && tile == 0 && a.update && a.slots &&
-                    __any_sync(0xffffffffu, slot_taken(a.slots, a.cu, n, slot, lane, 32)))
+                    __any_sync(0xffffffffu, slot_taken(a.slots, a.cu, a.total, n, slot, lane, 32)))
                     run = false;
                 float kk = 0.f, qq = 0.f;
                 kq = 0.f;
@@ -405,8 +405,9 @@ decode_chunks_kernel(RunsArgs a, int row_blocks, int tiles) {
                 }
                 if (tile == 0 && c0 == t0) {
                     // of the sequences with tokens that name one slot the first has it
-                    const int taken = run && a.update && a.slots
-                                          ? slot_taken(a.slots, a.cu, n, slot, tid, blockDim.x) : 0;
+                    const int taken =
+                        run && a.update && a.slots
+                            ? slot_taken(a.slots, a.cu, a.total, n, slot, tid, blockDim.x) : 0;
                     if (__syncthreads_or(taken)) run = false;
                     if (!run) {  // a row of padding: its outputs are zero, nothing else is touched
                         if (op)

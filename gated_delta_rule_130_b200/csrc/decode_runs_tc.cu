@@ -184,7 +184,7 @@ decode_chunks_tc_kernel(RunsArgs a, int row_blocks) {
         if (c0 == t0) {
             // of the sequences with tokens that name one slot the first has it
             const int taken = run && a.update && a.slots
-                                  ? slot_taken(a.slots, a.cu, n, slot, tid, blockDim.x) : 0;
+                                  ? slot_taken(a.slots, a.cu, a.total, n, slot, tid, blockDim.x) : 0;
             if (__syncthreads_or(taken)) run = false;
             if (!run) {  // a row of padding: its outputs are zero, nothing else is touched
                 if (op)

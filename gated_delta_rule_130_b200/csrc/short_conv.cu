@@ -247,7 +247,7 @@ conv_fwd(ConvArgs a, unsigned ctiles, int tile) {
                 if (s[k] < 0) continue;
                 const int at = table.find(s[k]), held_by = table.place[at];
                 if (held_by >= 0 && held_by < kTaken && m + k < seq[held_by] &&
-                    (!a.cu || a.cu[m + k] < a.cu[m + k + 1]))
+                    has_tokens(a.cu, a.total, m + k))
                     atomicOr(&table.place[at], kTaken);
             }
         }
@@ -412,7 +412,7 @@ conv_few(ConvArgs a, unsigned ctiles) {
     // of the sequences with tokens that name one slot the first has it
     bool zero = padding;
     if (held && a.slots) {
-        zero = __any_sync(0xffffffffu, slot_taken(a.slots, a.cu, n, slot, lane, 32));
+        zero = __any_sync(0xffffffffu, slot_taken(a.slots, a.cu, a.total, n, slot, lane, 32));
     }
     if (!live) return;
     const int p = part_of(a, cc);

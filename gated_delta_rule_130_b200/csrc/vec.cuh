@@ -204,10 +204,15 @@ __device__ __forceinline__ void load_slots(const int *slots, int i, int n, int (
 #pragma unroll
     for (int k = 0; k < 4; ++k) s[k] = i + k < n ? slots[i + k] : -1;
 }
+// Whether sequence i has tokens: offsets that are none leave it out, and the slot that it
+// names to the others.
+__device__ __forceinline__ bool has_tokens(const int *cu, int total, int i) {
+    return !cu || (cu[i] >= 0 && cu[i] < cu[i + 1] && cu[i + 1] <= total);
+}
 // Whether one of the sequences before n that have tokens names `slot` (>= 0); each caller
 // looks at its share.
-__device__ __forceinline__ int slot_taken(const int *slots, const int *cu, int n, int slot, int from,
-                                          int step) {
+__device__ __forceinline__ int slot_taken(const int *slots, const int *cu, int total, int n, int slot,
+                                          int from, int step) {
     int taken = 0;
 #pragma unroll 2
     for (int i = 4 * from; i < n; i += 4 * step) {
@@ -215,7 +220,7 @@ __device__ __forceinline__ int slot_taken(const int *slots, const int *cu, int n
         load_slots(slots, i, n, s);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (s[k] == slot) taken |= !cu || cu[i + k] < cu[i + k + 1];
+            if (s[k] == slot) taken |= has_tokens(cu, total, i + k);
     }
     return taken;
 }

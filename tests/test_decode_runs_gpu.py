@@ -299,3 +299,14 @@ def test_a_pool_beyond_32_bit_offsets(gdn):
                  torch.zeros(6, 1, D))
     R.close(o, ref[0], ref[2], roundings(3, D))
     R.close(states[use], ref[1], ref[3], roundings(3, D))
+
+
+@pytest.mark.parametrize("dtype,Dk,behind", [(F32, 32, 0), (F32, 32, 8), (BF16, 64, 0), (BF16, 64, 8), (BF16, 40, 8)])
+def test_sequences_left_out_keep_no_slot(gdn, dtype, Dk, behind):
+    # offsets before the first token, behind the last, decreasing: such a sequence does not hold
+    # the slot that it names (token by token, up to 8 at once, on the tensor cores)
+    d = draw(12, 1, 2, Dk, 24, 5, dtype, 25, behind=behind)
+    cu = [-3, 2, 5, 99, 8, 12]  # 2..5 and 8..12 run
+    o, S = check(gdn, d, cu, [0, 0, 1, 3, 1], dtype)
+    assert (o[2:5] != 0).any() and (o[8:12] != 0).any() and (o[5:8] == 7).all()
+    assert not torch.equal(S[0], d["states"][0]) and not torch.equal(S[1], d["states"][1])

@@ -282,3 +282,23 @@ def test_a_given_workspace(gdn):
         ws = torch.full((need + 64,), 7, dtype=torch.uint8, device="cuda")
         b = gdn.short_conv_bwd(d["dy"], d["x"], d["w"], d["b"], cu_seqlens=cu, workspace=ws[:size])
         assert all(torch.equal(s, t) for s, t in zip(a, b)) and (ws[size:] == 7).all()
+
+
+@pytest.mark.parametrize("tokens", [12, 5000])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_offsets_outside_the_tokens(gdn, tokens, dtype):
+    # a sequence that begins before the tokens and one that ends behind them are left out, and
+    # the slots that they name are free for the others
+    lens = [3] * ((tokens - 5) // 3)
+    cu = [-3, 2] + [2 + a for a in offsets(lens)[1:]] + [tokens + 4]
+    n = len(cu) - 1
+    slots = [1, 1] + list(range(2, n - 1)) + [0]
+    d = draw(tokens, 64, 4, n, dtype, 23)
+    y, S = check_fwd(gdn, d, cu, slots)
+    assert (y[:2] == 7).all() and (y[2:5] != 0).any() and not torch.equal(S[1], d["states"][1])
+    d = dict(d, b=None)
+    got = gdn.short_conv_bwd(d["dy"], d["x"], d["w"], cu_seqlens=dev(cu))
+    ref = R.conv_grads(d["dy"], d["x"], d["w"], None, cu, True)
+    R.close(got[0], ref[0], ref[3], bwd_roundings(tokens))
+    R.close(got[1], ref[1], ref[4], bwd_roundings(tokens))
+    assert (got[0][:2] == 0).all()
