@@ -543,14 +543,8 @@ def _call(dev: int, f, *args):
 
 
 def _like_parts(x, shapes):
-    """New arrays of x's type and device, from one allocation where they are alike and each
-    keeps a 16-byte boundary."""
-    first = shapes[0]
-    n = 1
-    for k in first:
-        n *= k
-    if len(shapes) > 1 and n % 8 == 0 and all(s == first for s in shapes):
-        return x.new_empty((len(shapes), *first)).unbind(0)
+    """New arrays of x's type and device, each of its own: views of one allocation would keep
+    one another alive and share autograd's count of changes in place."""
     return tuple([x.new_empty(s) for s in shapes])
 
 

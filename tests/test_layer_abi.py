@@ -324,3 +324,17 @@ def test_what_a_call_allocates_lives_until_the_entry_point_returns(monkeypatch, 
     passed.clear()
     b.rms_norm_bwd(z(4, 8), z(4, 8), z(8), workspace=ws)
     assert passed == [True] * 3  # dx, dweight, workspace
+
+
+def test_outputs_of_one_call_are_arrays_of_their_own():
+    # q, k and v (or dx and dgate) share neither memory, so that keeping one does not keep the
+    # others, nor a version counter, so that each may be changed in place beside the others
+    from gated_delta_rule_130_b200 import binding as b
+    scale = torch.ones(8, requires_grad=True)
+    for shapes in ([(4, 8)] * 3, [(4, 8), (4, 16)], [(4, 8)]):
+        made = b._like_parts(torch.zeros(2, dtype=torch.bfloat16), shapes)
+        assert [t.shape for t in made] == shapes and all(t.dtype == torch.bfloat16 for t in made)
+        assert all(t._base is None for t in made)
+        assert len({t.untyped_storage().data_ptr() for t in made}) == len(made)
+        made[0].mul_(scale)
+        assert all(t._version == 0 and not t.requires_grad for t in made[1:])
