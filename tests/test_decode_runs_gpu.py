@@ -310,3 +310,58 @@ def test_sequences_left_out_keep_no_slot(gdn, dtype, Dk, behind):
     o, S = check(gdn, d, cu, [0, 0, 1, 3, 1], dtype)
     assert (o[2:5] != 0).any() and (o[8:12] != 0).any() and (o[5:8] == 7).all()
     assert not torch.equal(S[0], d["states"][0]) and not torch.equal(S[1], d["states"][1])
+
+
+# ---- blocks that take several tiles of a head's rows: 296 (sequence, head) pairs and more
+
+def many(lens, Hv, Dk, Dv, dtype, seed):
+    n = len(lens)
+    assert n * Hv >= 296
+    d = draw(sum(lens), Hv // 2, Hv, Dk, Dv, n + 2, dtype, seed)
+    slots = torch.randperm(n + 2, generator=torch.Generator().manual_seed(seed)).tolist()[:n]
+    for i in range(0, n, 9):  # rows of padding, slots behind the pool, slots again
+        slots[i] = [-1, n + 2, slots[i // 2]][i // 9 % 3]
+    return d, offsets(lens), slots
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("Dk,Dv", [(128, 72), (16, 300), (256, 33), (96, 70), (33, 140)])
+def test_row_tiles_of_single_tokens(gdn, Dk, Dv, dtype):
+    lens = [1] * 74
+    lens[3] = lens[40] = 2  # a run of more than one token among them
+    d, cu, slots = many(lens, 4, Dk, Dv, dtype, Dk + Dv)
+    check(gdn, d, cu, slots, dtype)
+    check(gdn, d, cu, None, dtype, update=False)
+
+
+@pytest.mark.parametrize("dtype,Dk,Dv", [(F32, 128, 72), (F32, 16, 300), (F32, 256, 36), (F32, 37, 140),
+                                         (BF16, 72, 72), (BF16, 256, 36), (BF16, 128, 136), (BF16, 64, 144)])
+def test_row_tiles_of_runs(gdn, dtype, Dk, Dv):
+    lens = [2] * 74
+    lens[5], lens[6], lens[7], lens[50] = 9, 1, 17, 8
+    d, cu, slots = many(lens, 4, Dk, Dv, dtype, Dk + Dv)
+    check(gdn, d, cu, slots, dtype)
+    check(gdn, d, cu, None, dtype, update=False)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("Dk,Dv", [(33, 40), (130, 65), (200, 24), (255, 7), (256, 256), (1, 1)])
+def test_single_tokens_of_any_width(gdn, Dk, Dv, dtype):
+    d = draw(9, 1, 2, Dk, Dv, 7, dtype, Dk, behind=2)
+    check(gdn, d, [0, 1, 2, 2, 3, 5, 6, 7, 8, 9], [6, 0, 1, -1, 3, 4, 5, 2, 9], dtype)
+    check(gdn, d, [0, 1, 2, 2, 3, 5, 6, 7, 8, 9], [6, 0, 1, 3, 3, 4, 5, 2, 2], dtype, update=False)
+
+
+@pytest.mark.parametrize("dtype,Dk", [(F32, 64), (BF16, 128), (BF16, 64), (F32, 30)])
+def test_an_infinite_query_stays_with_its_token(gdn, dtype, Dk):
+    # its own outputs are infinite or NaN, all others and the states bit for bit what they were
+    d = draw(16, 1, 1, Dk, 32, 2, dtype, 24)
+    run = lambda S: gdn.decode_runs(d["q"], d["k"], d["v"], d["la"], d["be"], S,
+                                    cu_seqlens=torch.tensor([0, 8, 16], dtype=torch.int32, device="cuda"))
+    S, S2 = d["states"].clone(), d["states"].clone()
+    a = run(S)
+    d["q"][3, 0, 5] = float("inf")
+    b = run(S2)
+    assert torch.equal(S, S2) and not torch.isfinite(b[3]).any()
+    rest = [t for t in range(16) if t != 3]
+    assert torch.equal(a[rest], b[rest])
