@@ -302,3 +302,74 @@ def test_offsets_outside_the_tokens(gdn, tokens, dtype):
     R.close(got[0], ref[0], ref[3], bwd_roundings(tokens))
     R.close(got[1], ref[1], ref[4], bwd_roundings(tokens))
     assert (got[0][:2] == 0).all()
+
+
+# ---- the kernel over tiles of tokens, which calls of few blocks do not reach
+
+def mixed(total, seed):
+    """Lengths that begin and end sequences at every place of a tile and reach over tiles."""
+    g = torch.Generator().manual_seed(seed)
+    kinds = [0, 1, 1, 2, 2, 3, 4, 5, 7, 8, 9, 17, 40, 300]
+    lens = []
+    while sum(lens) < total:
+        lens.append(min(kinds[int(torch.randint(len(kinds), (1,), generator=g))], total - sum(lens)))
+    return lens
+
+
+def tiled(C, total, vec):
+    """Whether a forward of these sizes goes by tiles (more blocks than a batch of few tokens has)."""
+    return -(-C // (128 * vec)) * total > 148 * 32
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("C,total", [(36, 4999), (1032, 5003), (37, 5001), (1029, 4801)])
+def test_tiles(gdn, C, total, W, dtype):
+    assert tiled(C, total, 4)
+    lens = mixed(total, C + W)
+    n = len(lens)
+    g = torch.Generator().manual_seed(W)
+    slots = torch.randperm(n, generator=g).tolist()
+    for i in range(0, n, 11):      # rows of padding, slots behind the pool, slots again
+        slots[i] = [-1, n, slots[i // 2]][i // 11 % 3]
+    d = draw(total, C, W, n, dtype, C + W)
+    cu = offsets(lens)
+    check_fwd(gdn, d, cu, slots)
+    check_fwd(gdn, dict(d, b=None), cu, None, silu=False)
+    check_fwd(gdn, d, cu, None, silu=False, pool=False)
+    splits = [C // 3, C // 3, C - 2 * (C // 3)]
+    check_fwd(gdn, d, cu, slots, splits=splits)
+    check_fwd(gdn, dict(d, b=None), cu, None, splits=[C - 8, 8], pool=False)
+
+
+def test_high_tiles(gdn):
+    # tiles of more tokens than a block has threads, sequences around their edges
+    C, total = 6144, 12000
+    lens = mixed(total, 5)
+    d = draw(total, C, 4, len(lens), BF16, 21, bias=False)
+    slots = torch.randperm(len(lens), generator=torch.Generator().manual_seed(3)).tolist()
+    check_fwd(gdn, d, offsets(lens), slots)
+
+
+@pytest.mark.parametrize("lens", [[15, 1, 16, 17, 14, 2, 2, 4750], [7] * 700, [8] * 620, [3] * 1600, [4800, 7]])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_tile_edges_of_many_tokens(gdn, lens, dtype):
+    assert tiled(64, sum(lens), 4)
+    d = draw(sum(lens), 64, 4, len(lens), dtype, len(lens), bias=False)
+    slots = torch.randperm(len(lens), generator=torch.Generator().manual_seed(3)).tolist()
+    check_fwd(gdn, d, offsets(lens), slots)
+
+
+@pytest.mark.parametrize("dtype,C,W", [(F32, 1032, 4), (BF16, 1032, 4), (F32, 37, 3), (BF16, 1029, 2), (BF16, 36, 4)])
+def test_gradients_of_many_tokens(gdn, dtype, C, W):
+    total = 5003
+    lens = mixed(total, W)
+    d = draw(total, C, W, 1, dtype, C + W)
+    cu = offsets(lens)
+    for silu in (True, False):
+        got = gdn.short_conv_bwd(d["dy"], d["x"], d["w"], d["b"], cu_seqlens=dev(cu), silu=silu)
+        ref = R.conv_grads(d["dy"], d["x"], d["w"], d["b"], cu, silu)
+        for a, want, scale in zip(got, ref[:3], ref[3:]):
+            R.close(a, want, scale, bwd_roundings(total))
+        again = gdn.short_conv_bwd(d["dy"], d["x"], d["w"], d["b"], cu_seqlens=dev(cu), silu=silu)
+        assert all(torch.equal(a, b) for a, b in zip(got, again))
