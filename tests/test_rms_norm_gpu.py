@@ -249,3 +249,52 @@ def test_a_given_workspace(gdn):
         ws = torch.full((need + 64,), 7, dtype=torch.uint8, device="cuda")
         b = gdn.rms_norm_bwd(d["dy"], d["x"], d["w"], gate=d["gate"], workspace=ws[:size])
         assert all(torch.equal(s, t) for s, t in zip(a, b)) and (ws[size:] == 7).all()
+
+
+# 4736 rows and more take other splits of a row over threads than few rows do
+@pytest.mark.parametrize("shape,dtype", [((4736, 1032), BF16), ((4800, 2048), BF16), ((4737, 2056), BF16),
+                                         ((4736, 4096), BF16), ((4736, 516), F32), ((4741, 1024), F32),
+                                         ((4736, 2048), F32)])
+def test_forward_of_many_rows(gdn, shape, dtype):
+    d = draw(shape, dtype, shape[-1])
+    D = shape[-1]
+    for res, gate in ((None, None), (d["res"], None), (None, d["gate"])):
+        ref, href = R.norm(d["x"], d["w"], res, gate, EPS)
+        y, _, h = gdn.rms_norm_fwd(d["x"], d["w"], residual=res, gate=gate, eps=EPS)
+        R.close(y, ref, ref.abs(), roundings(D))
+        assert res is None or torch.equal(h.cpu(), href.cpu())
+        for quant in ("row", "group") if D % 128 == 0 else ("row",):
+            y, scale, h = gdn.rms_norm_fwd(d["x"], d["w"], residual=res, gate=gate, eps=EPS, quant=quant)
+            assert res is None or torch.equal(h.cpu(), href.cpu())
+            group = D if quant == "row" else 128
+            parts = ref.unflatten(-1, (-1, group))
+            top = parts.abs().amax(-1)
+            R.close(scale, top / 448, top / 448, roundings(D) + 2)
+            # as in test_eight_bits
+            value = y.float().cpu().double().unflatten(-1, (-1, group)) * scale.cpu().double()[..., None]
+            want = parts / (top / 448)[..., None]
+            bound = (want.abs() * 2.0 ** -4).clamp_min(2.0 ** -10)
+            bound = (bound + want.abs() * (roundings(D) + 4) * R.U32) * (top / 448)[..., None] * 1.001
+            assert ((value - parts).abs() <= bound).all()
+
+
+# rows for two rounds and more of the blocks that fit at once, with an uneven last one: the
+# next row's loads, the sums' two places and the row groups of a block are used again
+@pytest.mark.parametrize("rows,D,dtype", [
+    (60000, 32, BF16), (30001, 64, BF16), (15003, 128, BF16), (8005, 256, BF16), (5007, 512, BF16),
+    (1609, 1024, BF16), (1613, 2048, BF16), (700, 4096, BF16), (331, 8192, BF16), (311, 16384, BF16),
+    (1901, 1001, BF16), (60000, 16, F32), (30001, 32, F32), (15003, 64, F32), (8005, 128, F32),
+    (5007, 200, F32), (1609, 512, F32), (1613, 1000, F32), (700, 2048, F32), (331, 4096, F32),
+    (311, 8192, F32), (1901, 77, F32)])
+def test_gradients_of_many_rows(gdn, rows, D, dtype):
+    d = draw((rows, D), dtype, D + 3)
+    for gate, dres in ((None, d["dres"]), (d["gate"], None)):
+        dx, dw, dg = gdn.rms_norm_bwd(d["dy"], d["x"], d["w"], gate=gate, d_res=dres, eps=EPS)
+        ref = R.norm_grads(d["dy"], d["x"], d["w"], gate, dres, EPS)
+        c = bwd_roundings(D, rows)
+        R.close(dx, ref[0], ref[3], c)
+        R.close(dw, ref[1], ref[4], c)
+        if gate is not None:
+            R.close(dg, ref[2], ref[5] + 1e-30, c)
+        again = gdn.rms_norm_bwd(d["dy"], d["x"], d["w"], gate=gate, d_res=dres, eps=EPS)
+        assert all(a is b is None or torch.equal(a, b) for a, b in zip((dx, dw, dg), again))
