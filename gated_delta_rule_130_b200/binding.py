@@ -660,7 +660,8 @@ def short_conv_fwd(x, weight, bias=None, cu_seqlens=None, states=None, slots=Non
     2..4, and bias [C] float32 or x's type.  ``splits``: up to three widths that sum to
     C; y is then a tuple of arrays of these widths (q, k and v from one call).
     ``states`` [n_slots, W - 1, C] in x's type: the last inputs of each sequence, used
-    in front of it and replaced; ``slots`` and ``cu_seqlens`` as in ``decode_runs``.
+    in front of it and always replaced; ``slots`` and ``cu_seqlens`` as in ``decode_runs``,
+    except that the offsets must not decrease (valid sequences may then be left out).
     Without states sequences start from zero.  Rows of no sequence are not written: they
     keep what ``out`` held.
     """

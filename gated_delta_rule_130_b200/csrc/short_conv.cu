@@ -2,7 +2,9 @@
 //     z[t, c] = bias[c] + sum_j w[c, j] x[t - (W - 1) + j, c],   y = silu(z) or z,
 // W in 2..4, over sequences packed along the tokens; the inputs before a sequence
 // come from its slot of a pool of the last W - 1 inputs (which then takes the
-// sequence's own last ones) or are zero.  Backward, for sequences from zero:
+// sequence's own last ones) or are zero.  A token's sequence is found by bisection of the
+// offsets: where they decrease, valid sequences may be left out (nothing outside the arrays is
+// touched, and a slot still belongs to one sequence).  Backward, for sequences from zero:
 //     dz = dy silu'(z) or dy,   dx[t] = sum_j w[W - 1 - j] dz[t + j] (same sequence),
 //     dw[c, j] = sum_t dz[t] x[t - (W - 1) + j],   dbias = sum_t dz[t].
 //

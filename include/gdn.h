@@ -347,7 +347,10 @@ gdn_status_t gdn_decode_step_cw(const void *q, const void *k, const void *v,
  *    whose slot is not in [0, n_slots) is a row of padding: its outputs are zero
  *    and no state is touched.  So is, where states are written, a sequence with
  *    tokens whose slot an earlier sequence with tokens has.  Output rows that
- *    belong to no sequence keep what they held.
+ *    belong to no sequence keep what they held.  Of a row that several sequences
+ *    claim (offsets that decrease somewhere) it is not defined whose output it
+ *    holds.  The convolution finds a token's sequence by bisection: offsets that
+ *    decrease somewhere leave out sequences that are valid by themselves, too.
  */
 
 /*
