@@ -22,7 +22,7 @@
 //
 // Two kernels.  Token by token, for batches of short runs (decode): bound by HBM, the
 // state being read and written once; one token each of 256 sequences of 16 heads of
-// 128 x 128, 541 MB: 93.0 us on B200, 0.89 of the measured copy rate.  Up to 8 tokens at
+// 128 x 128, 541 MB: 91.7 us on B200, 0.90 of the measured copy rate.  Up to 8 tokens at
 // once, for longer runs: bound by the issue of its products' reductions and by the
 // barriers between its phases; 8 tokens of 256 sequences of 16 heads in float32: 182 us
 // (token by token 412 us).  bf16 runs of Dk = 64 or 128 go to decode_runs_tc.cu.  Where
@@ -31,7 +31,7 @@
 // 185 and about 120 for any number.
 //
 // Token by token each warp looks for its slot among the earlier sequences' by itself; for
-// 1024 sequences of 16 heads that is 336 us instead of 329, for 4096 1500 instead of 1290.
+// 1024 sequences of 16 heads that is 341 us instead of 328, for 4096 1483 instead of 1283.
 // Shared by the block it needs a barrier between the loads and the products: 348 and 1395
 // us, and 96 instead of 91 at 256.
 #include "runs_common.cuh"
@@ -538,11 +538,17 @@ Cover cover(const RunsArgs &a, int rows) {
 }
 
 // About two tokens per sequence or more on average: up to 8 tokens at once, else token by
-// token.  The figures are above and, for few sequences (us token by token and at once, bf16,
-// 16 heads of 128 x 128): 8 of 2 tokens 8.2 and 7.1 (float32 7.7 and 7.1), one of 1 token 3.5
-// and 6.6, of 3 6.6 and 6.8, of 4 8.1 and 6.9.  The host knows the sizes alone, not the
-// offsets, and a batch's rows behind its last sequence count too: for few sequences, of
-// which they can be most, the 4 allows for them.
+// token.  The figures for many sequences are above.  The host knows the sizes alone, not the
+// offsets: of a buffer of `total` rows any number from N on may belong to sequences.  For few
+// sequences the 4 sets the border where either mistake costs about the same.  In us, token by
+// token and at once, bf16, 16 heads of 128 x 128: one sequence of 1 token 3.6 and 6.7, of 3
+// 6.7 and 6.9, of 4 8.3 and 6.8, of 5 9.7 and 6.9 (float32 1 token 3.7 and 6.0, 5 tokens 7.4
+// and 7.1); 4 sequences of 1 token 4.7 and 7.1, of 2 6.3 and 7.2; 7 sequences of 1 token 5.6
+// and 7.2, of 2 8.0 and 7.3; 8 sequences of 1 token 5.9 and 7.3, of 2 8.2 and 7.1.  So a
+// sequence of 4 or 5 tokens in a buffer of its own size loses 3 us at most, a single token in
+// a buffer of 6 rows or more as much.  The average also knows nothing of a mixed batch: one
+// run of 400 tokens among 511 of one token goes token by token and takes 2913 us, at once it
+// would be 276 (float32 1976 and 691), as two calls 352.
 bool many_tokens(const RunsArgs &a) {
     return a.total >= 2ll * a.N - a.N / 8 + (a.N < 8 ? 4 : 1);
 }

@@ -14,8 +14,8 @@
 // update.  8 x 8 token products are far too small for a tcgen05 tile of 64 or 128 rows
 // with its round trip through tensor memory.
 //
-// 64 runs of 1 to 8 tokens against 32 value heads of 128 x 128 (read only, 135 MB): 42.4
-// us on B200, 0.49 of the measured copy rate (in float32 arithmetic 61.5 us); 8 tokens of
+// 64 runs of 1 to 8 tokens against 32 value heads of 128 x 128 (read only, 135 MB): 42.7
+// us on B200, 0.48 of the measured copy rate (in float32 arithmetic 61.5 us); 8 tokens of
 // 256 sequences of 16 heads, states written, 571 MB: 122.5 us, 0.71.  Two blocks of 128
 // registers a thread per SM; what bounds it is the chain of one part of the work -
 // offsets and slot, k and q, the tokens' products and the substitution on one warp, the
@@ -31,8 +31,9 @@
 // sequences of 16 heads), but spills where such a run is longer than 8 tokens; the split
 // into three parts and its products are then what it waits for (one part alone: 34).
 //
-// A state with an infinity gives NaN in its row, where the recurrence might give an
-// infinity.
+// An infinity does not split into three parts: it meets their zeros and differences and comes
+// out as NaN.  One in the state or in v gives NaN in its row, one in q in its token's outputs,
+// one in k from its token on, where the recurrence might give an infinity.
 #include "runs_common.cuh"
 
 namespace gdn {

@@ -12,9 +12,9 @@
 // vectors of 16 bytes each; sums are float32.
 //
 // On B200, bf16: 16384 rows of 2048 with residual to e4m3 39.1 us (235 MB, 0.92 of the
-// measured copy rate); 262144 gated rows of 128 35.6 us (201 MB, 0.86); gradients of
-// 16384 x 2048 with d_res 55 us (268 MB, 0.74, 5 us of it the sum over the blocks), of
-// the gated rows 72 us (336 MB, 0.71).
+// measured copy rate); 262144 gated rows of 128 35.9 us (201 MB, 0.86); gradients of
+// 16384 x 2048 with d_res 54 us (268 MB, 0.76, 4 us of it the sum over the blocks), of
+// the gated rows 68 us (336 MB, 0.75).
 #include <cuda_fp8.h>
 
 #include "kernels.h"

@@ -14,10 +14,10 @@
 // before a tile are read again.  Sums are float32; dw is summed per tile and then over
 // the tiles, in one order.
 //
-// On B200, bf16, W = 4, 12 sequences of 16384 tokens, 6144 channels: forward 73 us (403
-// MB, 0.84 of the measured copy rate), backward 119 us (604 MB, 0.77; 120 registers leave
+// On B200, bf16, W = 4, 12 sequences of 16384 tokens, 6144 channels: forward 74.5 us (403
+// MB, 0.82 of the measured copy rate), backward 119 us (604 MB, 0.77; 120 registers leave
 // 16 warps per SM, and it issues 23 instructions per element); one token each of 256
-// sequences 10.7 us (25 MB: 2.6 rounds of blocks that wait for offsets, slot and held
+// sequences 10.9 us (25 MB: three rounds of blocks that wait for offsets, slot and held
 // inputs in turn).
 #include "kernels.h"
 #include "vec.cuh"

@@ -368,6 +368,12 @@ gdn_status_t gdn_decode_step_cw(const void *q, const void *k, const void *v,
  *   flags      : gdn_flag_t bits and GDN_FLAG_READ_ONLY: the states are read and
  *                not written (a draft's outputs before it is accepted; several
  *                sequences may then share a slot).
+ * The kernel (token by token, or up to 8 tokens at once) is chosen by the average
+ * total / N, the offsets being on the device: a long run among many single tokens
+ * is better given as a call of its own.  Several tokens at once form the
+ * recurrence's sums in another order, so that an infinity in q, k, v or a state may
+ * come out as NaN where the recurrence keeps an infinity; it reaches the same
+ * outputs and no others.
  * Limits: those of gdn_decode_step, Hv a multiple of Hk, N <= 65535,
  * total <= 2^30, N * Hv * Dv < 2^31, n_slots * Hv <= 2^40.  o and states overlap nothing else.
  */
